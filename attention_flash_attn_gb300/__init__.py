@@ -3,7 +3,8 @@ causal / sliding-window / packed-segment masks.
 
 Thin Python binding over the C ABI of ``libattn_gb300.so`` (include/attn_gb300.h):
 PyTorch supplies device memory and the current stream; every step of the forward and
-backward runs in the library's CUDA kernels.  The names follow the C entry points.
+backward runs in the library's CUDA kernels.  The names follow the C entry points.  cache.py
+binds include/attn_cache_gb300.h: attention over an 8-bit paged cache, its append and eviction.
 """
 from __future__ import annotations
 
@@ -14,10 +15,13 @@ import torch
 
 from . import _capi
 from ._capi import AttnArgs, AttnError, lib  # noqa: F401
+from .cache import (AttnCache, attn_cache_append, attn_cache_check_device_status, attn_cache_evict, attn_cache_fwd,
+                    attn_cache_path_name)
 
 __all__ = ["attn_fwd", "attn_fwd_noalloc", "attn_bwd", "attn_meta", "attn_check_device_status", "attn_path_name",
            "attn_launch_counter", "attn_profile_next_main_kernel", "attn_profile_next_aux_kernels", "AttnError",
-           "build_args"]
+           "build_args", "AttnCache", "attn_cache_append", "attn_cache_fwd", "attn_cache_evict",
+           "attn_cache_check_device_status", "attn_cache_path_name"]
 
 _DTYPES = {torch.bfloat16: _capi.ATTN_DTYPE_BF16, torch.float32: _capi.ATTN_DTYPE_F32}
 _ws_cache: dict = {}

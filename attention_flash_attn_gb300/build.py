@@ -38,7 +38,7 @@ def _sources():
 def _stamp() -> str:
     h = hashlib.sha256()
     files = _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")))
-    files.append(os.path.join(ROOT, "include", "attn_gb300.h"))
+    files += sorted(glob.glob(os.path.join(ROOT, "include", "*.h")))
     for f in files:
         h.update(os.path.relpath(f, ROOT).encode())  # relative: the same sources hash alike anywhere
         with open(f, "rb") as fh:

@@ -1,0 +1,213 @@
+// cache_common.cuh -- what the kernels of the 8-bit paged cache share: the cache's view, code
+// conversions, the scale rule, and the plan that spreads attention over the grid.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <limits.h>
+#include <math_constants.h>
+
+#include "../../include/attn_cache_gb300.h"
+#include "common.cuh"
+#include "internal.h"
+
+namespace attn {
+namespace cache {
+
+// Device status bits, beside those of common.cuh.
+enum : unsigned {
+  kStatusBadPage = 8u,        // a page id outside the cache, or a length outside the table
+  kStatusNonFinite = 16u,     // an appended value was infinite or NaN
+};
+
+// The cache and the sequences of a call, as kernels take them.
+struct View {
+  int num_pages, page_shift, page, Hkv, D;
+  uint8_t *k, *v;
+  float *k_scale, *v_scale;
+  unsigned *status;
+  int B, max_pages;
+  const int *table;
+  long long table_stride;
+  const int *lengths;
+};
+
+// Length of sequence b, brought into [0, table's end]; *bad is set when it was outside.
+__device__ __forceinline__ int seq_len(const View &c, int b, bool *bad) {
+  const int n = c.lengths[b];
+  const long long cap = (long long)c.max_pages << c.page_shift;
+  *bad = n < 0 || n > cap;
+  return n < 0 ? 0 : (int)(n > cap ? cap : n);
+}
+__device__ __forceinline__ int seq_len(const View &c, int b) {
+  bool bad;
+  return seq_len(c, b, &bad);
+}
+
+// Page that holds position pos of sequence b, or -1 (recorded) if its id is outside the cache.
+__device__ __forceinline__ int page_of(const View &c, int b, int pos) {
+  const int id = c.table[b * c.table_stride + (pos >> c.page_shift)];
+  if ((unsigned)id < (unsigned)c.num_pages) return id;
+  set_status(c.status, kStatusBadPage);
+  return -1;
+}
+
+// Row of codes (in elements) of slot `slot` of a page, for kv head h: 64-bit, as a cache may hold
+// more than 2^32 codes.
+__device__ __forceinline__ size_t row_at(const View &c, int page, int h, int slot) {
+  return ((((size_t)page * c.Hkv + h) << c.page_shift) + slot) * c.D;
+}
+
+constexpr int kMinScaleExp = -60;  // least scale 2^-60: smaller magnitudes round to coarser steps or 0
+constexpr float kMinScale = 8.673617379884035e-19f;
+
+template <int KIND> __device__ __forceinline__ constexpr float qmax() { return KIND == ATTN_CACHE_E4M3 ? 448.f : 127.f; }
+
+// The least power of two s >= 2^-60 with amax <= qmax * s (amax finite, >= 0): the exponent of
+// amax / qmax rounded up, taken from amax's own bits.  448 = 1.75 * 2^8 and 127 = 1.984375 * 2^6,
+// so amax = m * 2^e (1 <= m < 2) needs e - 8 (e - 6), and one more if m is above that mantissa.
+template <int KIND> __device__ __forceinline__ float need_scale(float amax) {
+  const unsigned u = __float_as_uint(amax);
+  const int e = (int)(u >> 23) - 127;  // below -126 for subnormals: the lower bound takes over
+  const unsigned m = u & 0x7fffffu;
+  int x = KIND == ATTN_CACHE_E4M3 ? e - 8 + (m > 0x600000u) : e - 6 + (m > 0x7e0000u);
+  if (x < kMinScaleExp) x = kMinScaleExp;
+  return __uint_as_float((unsigned)(x + 127) << 23);
+}
+
+// 1 / s for a power of two s in [2^-60, 2^120]: exact.
+__device__ __forceinline__ float pow2_inverse(float s) { return __uint_as_float(0x7f000000u - __float_as_uint(s)); }
+
+// Two codes from two values already in units of their scale: rounded to nearest even, saturated.
+template <int KIND> __device__ __forceinline__ unsigned encode2(float lo, float hi) {
+  if (KIND == ATTN_CACHE_E4M3) {
+    unsigned short r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+  const int a = lo == lo ? __float2int_rn(fminf(fmaxf(lo, -127.f), 127.f)) : 0;
+  const int b = hi == hi ? __float2int_rn(fminf(fmaxf(hi, -127.f), 127.f)) : 0;
+  return (a & 0xff) | ((b & 0xff) << 8);
+}
+
+// Two codes widened to fp16: exact for both kinds (e4m3 has fewer bits and a smaller range, int8
+// has 8 bits).
+template <int KIND> __device__ __forceinline__ unsigned decode2_h(unsigned codes) {
+  unsigned r;
+  if (KIND == ATTN_CACHE_E4M3) {
+    asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(r) : "r"(codes));
+  } else {
+    const __half2 h = __halves2half2(__int2half_rn((int)(signed char)(codes & 0xff)),
+                                     __int2half_rn((int)(signed char)((codes >> 8) & 0xff)));
+    r = *reinterpret_cast<const unsigned *>(&h);
+  }
+  return r;
+}
+template <int KIND> __device__ __forceinline__ float2 decode2(unsigned codes) {
+  const unsigned h = decode2_h<KIND>(codes);
+  return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+// Four codes of a word.
+template <int KIND> __device__ __forceinline__ void decode4(unsigned w, float *x) {
+  if (KIND == ATTN_CACHE_E4M3) {
+    const float2 a = decode2<KIND>(w & 0xffffu), b = decode2<KIND>(w >> 16);
+    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = (float)(int)(signed char)(w >> (8 * i));
+  }
+}
+
+// Maximum that keeps a NaN, so that a row with a NaN logit ends as NaN and not as an empty row.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// ---------------------------------------------------------------- attention
+
+struct FwdParams {
+  View c;
+  int Sq, Hq, G, R;      // R = G * Sq: query rows of one (sequence, kv head); row r is query r / G,
+                         // head h * G + r % G
+  int row_tile, NG, RT;  // rows per work item; RT = ceil(R / row_tile); NG = B * RT groups (b, tile)
+  int max_ctas;
+  int causal, window;
+  float cap, inv_cap, scale;
+  const void *q;
+  long long q_sb, q_ss, q_sh;
+  const float *sink;
+  int off_by_one;
+  void *O;
+  float *LSE;
+  const float *w_in;
+  float *w_out;
+  long long w_sb, w_sh;
+  // workspace
+  long long *prefix;     // [NG + 1]: units of the groups before each; prefix[NG]: units of one kv head
+  float *o_part;         // [2 * max_ctas, row_tile, D]: unnormalised partial outputs
+  float2 *ml_part;       // [2 * max_ctas, row_tile]: exponent reference (base 2) and sum
+  float *scores;         // [B * Hkv, R, Lpad]: logits times log2(e), -inf where unseen
+  long long Lpad;
+};
+
+constexpr int kUnit = 128;  // keys of one unit of work: four warps of 32
+
+// The keys [lo, hi) that some row of a group's tile sees; lo rounded down to 32 keys (slices of a
+// warp start on multiples of 32, so that they lie in one page, or in whole pages of 16).
+struct Range {
+  int lo, hi, len;
+};
+__device__ __forceinline__ Range group_range(const FwdParams &p, int b, int rt) {
+  Range g;
+  g.len = seq_len(p.c, b);
+  const int r0 = rt * p.row_tile, r1 = min(p.R, r0 + p.row_tile) - 1;
+  const long long first = (long long)g.len - p.Sq;  // position of query 0
+  const long long top = first + r1 / p.G, bottom = first + r0 / p.G;
+  g.hi = p.causal && top + 1 < g.len ? (int)(top + 1 < 0 ? 0 : top + 1) : g.len;
+  g.lo = 0;
+  if (p.window > 0 && bottom - p.window + 1 > 0) g.lo = (int)(bottom - p.window + 1) & ~31;
+  if (g.lo > g.hi) g.lo = g.hi;  // nothing to see
+  return g;
+}
+__device__ __forceinline__ int range_units(const Range &g) { return (g.hi - g.lo + kUnit - 1) / kUnit; }
+
+// First unit of CTA c's share of U units over C CTAs, and the CTA whose share holds unit u.
+__device__ __forceinline__ long long share_begin(long long c, long long U, long long C) { return c * U / C; }
+__device__ __forceinline__ long long share_owner(long long u, long long U, long long C) { return ((u + 1) * C - 1) / U; }
+__device__ __forceinline__ long long used_ctas(long long U, int max_ctas) { return U < max_ctas ? U : max_ctas; }
+
+// log2 of the exponentials' unit: logits are kept in base 2.
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+cudaError_t launch_fwd_simt(const FwdParams &p, int dtype, int kind, cudaStream_t st);
+cudaError_t launch_fwd_join(const FwdParams &p, int dtype, cudaStream_t st);
+cudaError_t launch_weights(const FwdParams &p, cudaStream_t st);
+
+struct AppendParams {
+  View c;
+  int S, span;  // span: pages that S tokens can touch
+  const void *k, *v;
+  long long k_sb, k_ss, k_sh, v_sb, v_ss, v_sh;
+  const int *counts;
+  int *lengths_out;
+  float *weights;
+  long long w_sb, w_sh;
+};
+cudaError_t launch_append(const AppendParams &p, int dtype, int kind, cudaStream_t st);
+
+struct EvictParams {
+  View c;
+  int keep, first, recent, out_pages;
+  const float *weights;
+  long long w_sb, w_sh;
+  const int *table_out;
+  long long table_out_stride;
+  int *kept, *lengths_out;
+  float *weights_out;
+};
+cudaError_t launch_evict(const EvictParams &p, int kind, cudaStream_t st);
+
+}  // namespace cache
+}  // namespace attn

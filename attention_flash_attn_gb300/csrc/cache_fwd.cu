@@ -1,0 +1,379 @@
+// cache_fwd.cu -- attention over the 8-bit cache on fp32 FFMA (fp32 queries, head dims without a
+// tensor-core kernel), and the kernels both paths end in: the join of split items and the
+// accumulation of attention weights.
+#include "cache_work.cuh"
+
+namespace attn {
+namespace cache {
+namespace {
+
+constexpr int kWarps = kThreads / 32;
+constexpr int kRows = 8;  // rows of a work item on this path
+
+template <typename T> __device__ __forceinline__ float4 load4f(const T *p);
+template <> __device__ __forceinline__ float4 load4f<float>(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+template <> __device__ __forceinline__ float4 load4f<__nv_bfloat16>(const __nv_bfloat16 *p) {
+  const uint2 u = *reinterpret_cast<const uint2 *>(p);
+  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.x));
+  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+template <typename T> __device__ __forceinline__ void store4f(T *p, float4 x);
+template <> __device__ __forceinline__ void store4f<float>(float *p, float4 x) { *reinterpret_cast<float4 *>(p) = x; }
+template <> __device__ __forceinline__ void store4f<__nv_bfloat16>(__nv_bfloat16 *p, float4 x) {
+  __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+  uint2 u;
+  u.x = *reinterpret_cast<uint32_t *>(&a);
+  u.y = *reinterpret_cast<uint32_t *>(&b);
+  *reinterpret_cast<uint2 *>(p) = u;
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x = max_nan(x, __shfl_xor_sync(~0u, x, o));
+  return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+  return x;
+}
+
+// Four warps; each takes every fourth slice of 32 keys of the CTA's run.  Scores: one key per
+// lane, its codes read 16 at a time and multiplied with the rows' queries broadcast from shared
+// memory.  Output: four columns per lane (of each 128), the slice's probabilities broadcast from
+// shared memory.  NC: 128-column parts of D.  Bound by FFMA: 2 * 2 * 8 rows * D per 2 * D bytes is
+// 16 flops a byte, above what the fp32 pipes give at the memory's rate.
+template <typename T, int KIND, int NC>
+__global__ void __launch_bounds__(kThreads) cache_fwd_simt_kernel(const __grid_constant__ FwdParams p) {
+  extern __shared__ __align__(16) float sm[];
+  const int D = p.c.D;
+  float *s_q = sm;                      // [kRows][D]
+  float *s_o = s_q + kRows * D;         // [kRows][D]
+  float *s_p = s_o + kRows * D;         // [kWarps][kRows][32]
+  float2 *s_ml = reinterpret_cast<float2 *>(s_p + kWarps * kRows * 32);  // [kWarps][kRows]
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  float *my_p = s_p + warp * kRows * 32;
+
+  Cursor cur;
+  if (!cursor_begin(p, cur)) return;
+  Run run;
+  while (cursor_next(p, cur, run)) {
+    const int r0 = run.rt * kRows, rows = min(kRows, p.R - r0);
+    __syncthreads();  // the previous run has left shared memory
+    for (int x = t; x < kRows * D / 4; x += kThreads) {
+      const int r = x / (D / 4), d = (x - r * (D / 4)) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < rows) {
+        const int i = (r0 + r) / p.G, h = run.hk * p.G + (r0 + r - i * p.G);
+        v = load4f(static_cast<const T *>(p.q) + run.b * p.q_sb + i * p.q_ss + h * p.q_sh + d);
+      }
+      *reinterpret_cast<float4 *>(s_q + r * D + d) = v;
+    }
+    __syncthreads();
+
+    float m[kRows], l[kRows], acc[kRows][NC][4];
+    long long pos_q[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      m[r] = -CUDART_INF_F;
+      l[r] = 0.f;
+      pos_q[r] = (long long)run.range.len - p.Sq + (r0 + r) / p.G;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) acc[r][c][x] = 0.f;
+    }
+    const int key0 = run.range.lo + run.off * kUnit, key1 = min(run.range.hi, key0 + run.cnt * kUnit);
+    for (int base = key0 + warp * 32; base < key1; base += kWarps * 32) {
+      const int pos = base + lane;
+      int page = -1;
+      if (pos < key1) page = page_of(p.c, run.b, pos);
+      const int slot = pos & (p.c.page - 1);
+      float s[kRows];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) s[r] = 0.f;
+      float ks = 0.f, lv = 0.f, inv = 1.f;
+      bool zero = true;
+      if (page >= 0) {
+        ks = p.c.k_scale[(size_t)page * p.c.Hkv + run.hk] * p.scale;
+        lv = scale_log2(p.c.v_scale[(size_t)page * p.c.Hkv + run.hk], &inv, &zero);
+        const uint4 *krow = reinterpret_cast<const uint4 *>(p.c.k + row_at(p.c, page, run.hk, slot));
+        for (int d = 0; d < D; d += 16) {
+          const uint4 w = krow[d >> 4];
+          const unsigned ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            float x[4];
+            decode4<KIND>(ww[y], x);
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+              const float4 q = *reinterpret_cast<const float4 *>(s_q + r * D + d + 4 * y);
+              s[r] = fmaf(q.x, x[0], fmaf(q.y, x[1], fmaf(q.z, x[2], fmaf(q.w, x[3], s[r]))));
+            }
+          }
+        }
+      }
+      bool all = true;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const bool vis = page >= 0 && r < rows && sees(p, pos_q[r], pos);
+        all = all && (vis || r >= rows);
+        float u = s[r] * ks;
+        if (p.cap > 0.f) u = p.cap * tanhf(u * p.inv_cap);
+        const float t2 = vis ? u * kLog2e : -CUDART_INF_F;
+        if (p.scores && r < rows) scores_row(p, run.b, run.hk, r0 + r)[pos] = t2;
+        const float e = t2 + lv;
+        const float mn = max_nan(m[r], warp_max(e));
+        float pr = 0.f, alpha = 1.f;
+        if (mn != -CUDART_INF_F) {
+          pr = vis ? exp2f(e - mn) : 0.f;
+          alpha = exp2f(m[r] - mn);
+        }
+        m[r] = mn;
+        l[r] = l[r] * alpha + pr * inv;
+        if (alpha != 1.f) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) acc[r][c][x] *= alpha;
+        }
+        my_p[r * 32 + lane] = zero ? 0.f : pr;
+      }
+      // Keys that some row does not see: their values are skipped for that row, not multiplied
+      // by 0 (a code may be NaN).
+      const bool skip0 = !__all_sync(~0u, all && !zero);
+      __syncwarp();
+      const int nk = min(32, key1 - base);
+      for (int kk = 0; kk < nk; ++kk) {
+        const int pg = __shfl_sync(~0u, page, kk);
+        if (pg < 0) continue;
+        const uint8_t *vrow = p.c.v + row_at(p.c, pg, run.hk, (base + kk) & (p.c.page - 1));
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const int d = c * 128 + lane * 4;
+          if (d < D) {
+            float x[4];
+            decode4<KIND>(*reinterpret_cast<const unsigned *>(vrow + d), x);
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+              const float pr = my_p[r * 32 + kk];
+              if (skip0 && pr == 0.f) continue;
+#pragma unroll
+              for (int y = 0; y < 4; ++y) acc[r][c][y] = fmaf(pr, x[y], acc[r][c][y]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+    }
+
+    // The four warps' rows joined in shared memory.
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const float lr = warp_sum(l[r]);
+      if (lane == 0) s_ml[warp * kRows + r] = make_float2(m[r], lr);
+    }
+    __syncthreads();
+    float f[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      float M = -CUDART_INF_F;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = max_nan(M, s_ml[w * kRows + r].x);
+      f[r] = m[r] == -CUDART_INF_F ? 0.f : exp2f(m[r] - M);
+    }
+    for (int w = 0; w < kWarps; ++w) {
+      if (warp == w) {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const int d = c * 128 + lane * 4;
+            if (d < D) {
+              float4 *o = reinterpret_cast<float4 *>(s_o + r * D + d);
+              float4 v = w ? *o : make_float4(0.f, 0.f, 0.f, 0.f);
+              if (f[r] != 0.f) {
+                v.x += f[r] * acc[r][c][0];
+                v.y += f[r] * acc[r][c][1];
+                v.z += f[r] * acc[r][c][2];
+                v.w += f[r] * acc[r][c][3];
+              }
+              *o = v;
+            }
+          }
+      }
+      __syncthreads();
+    }
+    const bool whole = run.cnt == run.n;
+    for (int r = warp; r < rows; r += kWarps) {
+      float M = -CUDART_INF_F, L = 0.f;
+      for (int w = 0; w < kWarps; ++w) M = max_nan(M, s_ml[w * kRows + r].x);
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 ml = s_ml[w * kRows + r];
+        if (ml.x != -CUDART_INF_F) L += ml.y * exp2f(ml.x - M);
+      }
+      float scale = 1.f;
+      if (whole) {
+        const RowEnd e = row_end(p, run.hk * p.G + (r0 + r) % p.G, M, L);
+        scale = e.scale;
+        if (lane == 0) p.LSE[lse_at(p, run.b, run.hk, r0 + r)] = e.lse;
+      } else if (lane == 0) {
+        p.ml_part[(size_t)run.slot * kRows + r] = make_float2(M, L);
+      }
+      for (int d = lane * 4; d < D; d += 128) {
+        float4 v = *reinterpret_cast<float4 *>(s_o + r * D + d);
+        if (whole) {
+          if (M == -CUDART_INF_F) v = make_float4(0.f, 0.f, 0.f, 0.f);
+          v.x *= scale; v.y *= scale; v.z *= scale; v.w *= scale;
+          store4f(static_cast<T *>(p.O) + o_row(p, run.b, run.hk, r0 + r) + d, v);
+        } else {
+          *reinterpret_cast<float4 *>(p.o_part + ((size_t)run.slot * kRows + r) * D + d) = v;
+        }
+      }
+    }
+  }
+}
+
+// One block per row of an item that is split (or empty): the parts' outputs weighted by
+// 2^(M_c - M), four parts at a time (one per warp), and the extra column added once.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) cache_join_kernel(const __grid_constant__ FwdParams p) {
+  __shared__ float4 s_o[kWarps][128];
+  __shared__ float2 s_ml[kWarps];
+  const int hk = blockIdx.x / p.NG, g = blockIdx.x - hk * p.NG, b = g / p.RT, rt = g - b * p.RT;
+  const int r = rt * p.row_tile + blockIdx.y;
+  if (r >= p.R) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = p.c.D;
+  const long long first = p.prefix[g], n = p.prefix[g + 1] - first, Uh = p.prefix[p.NG];
+  const long long U = Uh * p.c.Hkv, C = used_ctas(U, p.max_ctas), s = hk * Uh + first;
+  long long c0 = 0, c1 = -1;
+  if (n > 0) {
+    c0 = share_owner(s, U, C);
+    c1 = share_owner(s + n - 1, U, C);
+    if (c0 == c1) return;  // one CTA had the whole item
+  }
+  // The row's partial of CTA c: the item is the second of the first CTA's two if it begins behind
+  // that CTA's first unit, and the first of every later one's.
+  const int second = n > 0 && s > share_begin(c0, U, C) ? 1 : 0;
+  auto part = [&](long long c) { return (size_t)(2 * c + (c == c0 ? second : 0)) * p.row_tile + blockIdx.y; };
+  float M = -CUDART_INF_F;
+  for (long long c = c0 + threadIdx.x; c <= c1; c += kThreads) M = max_nan(M, p.ml_part[part(c)].x);
+  M = warp_max(M);
+  if (lane == 0) s_ml[warp].x = M;
+  __syncthreads();
+  M = max_nan(max_nan(s_ml[0].x, s_ml[1].x), max_nan(s_ml[2].x, s_ml[3].x));
+  float L = 0.f;
+  float4 acc[4];  // 512 columns
+#pragma unroll
+  for (int x = 0; x < 4; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (long long c = c0 + warp; c <= c1; c += kWarps) {
+    const size_t at = part(c);
+    const float2 ml = p.ml_part[at];
+    if (ml.x == -CUDART_INF_F) continue;
+    const float f = exp2f(ml.x - M);
+    L += ml.y * f;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int d = x * 128 + lane * 4;
+      if (d < D) {
+        const float4 v = *reinterpret_cast<const float4 *>(p.o_part + at * D + d);
+        acc[x].x += f * v.x; acc[x].y += f * v.y; acc[x].z += f * v.z; acc[x].w += f * v.w;
+      }
+    }
+  }
+  if (lane == 0) s_ml[warp].y = L;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) s_o[warp][x * 32 + lane] = acc[x];
+  __syncthreads();
+  L = (s_ml[0].y + s_ml[1].y) + (s_ml[2].y + s_ml[3].y);
+  const RowEnd e = row_end(p, hk * p.G + r % p.G, M, L);
+  if (threadIdx.x == 0) p.LSE[lse_at(p, b, hk, r)] = e.lse;
+  const int d = threadIdx.x * 4;
+  if (d < D) {
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (M != -CUDART_INF_F) {
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 v = s_o[w][threadIdx.x];
+        o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+      }
+      o.x *= e.scale; o.y *= e.scale; o.z *= e.scale; o.w *= e.scale;
+    }
+    store4f(static_cast<T *>(p.O) + o_row(p, b, hk, r) + d, o);
+  }
+}
+
+// weights_out = weights + sum over the rows of 2^(score - LSE): four keys per thread, the rows'
+// scores read as the attention kernel stored them, summed in row order.
+__global__ void __launch_bounds__(kThreads) cache_weights_kernel(const __grid_constant__ FwdParams p) {
+  const int b = blockIdx.x / p.c.Hkv, hk = blockIdx.x - b * p.c.Hkv;
+  const int len = seq_len(p.c, b);
+  const int j0 = (blockIdx.y * kThreads + threadIdx.x) * 4;
+  if (j0 >= len) return;
+  float w[4] = {0.f, 0.f, 0.f, 0.f};
+  const float *row = scores_row(p, b, hk, 0) + j0;
+  for (int r = 0; r < p.R; ++r, row += p.Lpad) {
+    const long long pos = (long long)len - p.Sq + r / p.G;
+    // Scores are stored for the keys that some row of the tile sees (a superset of these).
+    const bool some = (!p.causal || j0 <= pos) && (p.window <= 0 || pos - (j0 + 3) < p.window);
+    if (!some) continue;
+    const float lse2 = p.LSE[lse_at(p, b, hk, r)] * kLog2e;
+    const float4 s = *reinterpret_cast<const float4 *>(row);
+    const float t[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (j0 + x < len && sees(p, pos, j0 + x)) w[x] += t[x] == -CUDART_INF_F ? 0.f : exp2f(t[x] - lse2);
+  }
+  const size_t at = (size_t)b * p.w_sb + (size_t)hk * p.w_sh + j0;
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+    if (j0 + x < len) p.w_out[at + x] = p.w_in[at + x] + w[x];
+}
+
+template <typename T, int KIND>
+cudaError_t launch_simt_t(const FwdParams &p, cudaStream_t st) {
+  const int D = p.c.D;
+  const size_t smem = (size_t)(2 * kRows * D + kWarps * kRows * 32) * 4 + kWarps * kRows * 8;
+  auto go = [&](auto kernel) {
+    kernel<<<p.max_ctas, kThreads, smem, st>>>(p);
+    return counted(cudaGetLastError());
+  };
+  switch ((D + 127) / 128) {
+    case 1: return go(cache_fwd_simt_kernel<T, KIND, 1>);
+    case 2: return go(cache_fwd_simt_kernel<T, KIND, 2>);
+    case 3: return go(cache_fwd_simt_kernel<T, KIND, 3>);
+    default: return go(cache_fwd_simt_kernel<T, KIND, 4>);
+  }
+}
+
+}  // namespace
+
+int simt_row_tile() { return kRows; }
+
+cudaError_t launch_fwd_simt(const FwdParams &p, int dtype, int kind, cudaStream_t st) {
+  if (dtype == kF32)
+    return kind == ATTN_CACHE_E4M3 ? launch_simt_t<float, ATTN_CACHE_E4M3>(p, st) : launch_simt_t<float, ATTN_CACHE_INT8>(p, st);
+  return kind == ATTN_CACHE_E4M3 ? launch_simt_t<__nv_bfloat16, ATTN_CACHE_E4M3>(p, st)
+                                 : launch_simt_t<__nv_bfloat16, ATTN_CACHE_INT8>(p, st);
+}
+
+cudaError_t launch_fwd_join(const FwdParams &p, int dtype, cudaStream_t st) {
+  const dim3 grid((unsigned)(p.NG * p.c.Hkv), (unsigned)min(p.row_tile, p.R));
+  if (dtype == kF32)
+    cache_join_kernel<float><<<grid, kThreads, 0, st>>>(p);
+  else
+    cache_join_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(p);
+  return counted(cudaGetLastError());
+}
+
+cudaError_t launch_weights(const FwdParams &p, cudaStream_t st) {
+  const long long cap = (long long)p.c.max_pages << p.c.page_shift;
+  const dim3 grid((unsigned)(p.c.B * p.c.Hkv), (unsigned)((cap + 4 * kThreads - 1) / (4 * kThreads)));
+  cache_weights_kernel<<<grid, kThreads, 0, st>>>(p);
+  return counted(cudaGetLastError());
+}
+
+}  // namespace cache
+}  // namespace attn

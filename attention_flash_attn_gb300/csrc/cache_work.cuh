@@ -1,0 +1,176 @@
+// cache_work.cuh -- how attention over the cache is spread over the grid, and how a piece of work
+// ends.  Work items are (kv head, sequence, row tile); an item's keys are cut into units of 128,
+// and the units of all items, in that order, are shared out evenly over the CTAs: one long
+// sequence is split over the whole grid, many short ones are run several to a CTA, and ragged
+// batches balance.  A CTA turns each run of units of one item into either the item's result, if
+// it holds all of them, or a partial (exponent reference, sum, unnormalised output), which the
+// join kernel combines.  A CTA has at most two partials: that of the item it begins in, and that
+// of the item it ends in.
+//
+// Numbers.  With a value's scale 2^lv, a row keeps M >= max_j(t_j + lv_j) in base 2 and
+//   O' = sum_j 2^(t_j + lv_j - M) code_j,      l = sum_j 2^(t_j + lv_j - M) 2^-lv_j,
+// so the scale costs nothing per element of V and the 2^(..) fed to the MMA stay within (0, 1]
+// whatever the pages' scales; O = O' / l and LSE = ln2 (M + log2 l).
+#pragma once
+
+#include "cache_common.cuh"
+
+namespace attn {
+namespace cache {
+
+constexpr int kThreads = 128;
+
+// The units of a CTA, item by item.
+struct Cursor {
+  long long Uh;        // units of one kv head
+  long long u0, u, u1; // this CTA's units; u: the next one
+  int hk, g;           // item of unit u
+  long long g_first;   // first unit of that item
+};
+
+// A run of units [off, off + cnt) of item (hk, b, rt), which has n of them.
+struct Run {
+  int hk, b, rt, off, cnt, n, slot;  // slot: where a partial goes
+  Range range;
+};
+
+// Called by all kThreads threads; false if this CTA has no units.  CTA 0 stores the prefix sums and
+// records lengths outside the table.
+__device__ __forceinline__ bool cursor_begin(const FwdParams &p, Cursor &cur) {
+  __shared__ long long s_sum[kThreads / 32];
+  __shared__ long long s_first;
+  __shared__ int s_g;
+  const int t = threadIdx.x;
+  const int g0 = (int)((long long)t * p.NG / kThreads), g1 = (int)((long long)(t + 1) * p.NG / kThreads);
+  long long sum = 0;
+  for (int g = g0; g < g1; ++g) sum += range_units(group_range(p, g / p.RT, g % p.RT));
+  long long incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(~0u, incl, o);
+    if ((t & 31) >= o) incl += v;
+  }
+  if ((t & 31) == 31) s_sum[t >> 5] = incl;
+  __syncthreads();
+  long long before = 0, Uh = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < (t >> 5)) before += s_sum[w];
+    Uh += s_sum[w];
+  }
+  const long long excl = before + incl - sum;
+  if (blockIdx.x == 0) {
+    long long x = excl;
+    for (int g = g0; g < g1; ++g) {
+      p.prefix[g] = x;
+      x += range_units(group_range(p, g / p.RT, g % p.RT));
+    }
+    if (t == kThreads - 1) p.prefix[p.NG] = Uh;
+    for (int b = t; b < p.c.B; b += kThreads) {
+      bool bad;
+      seq_len(p.c, b, &bad);
+      if (bad) set_status(p.c.status, kStatusBadPage);
+    }
+  }
+  const long long U = Uh * p.c.Hkv, C = used_ctas(U, p.max_ctas);
+  if (blockIdx.x >= C) return false;
+  cur.Uh = Uh;
+  cur.u0 = cur.u = share_begin(blockIdx.x, U, C);
+  cur.u1 = share_begin(blockIdx.x + 1, U, C);
+  cur.hk = (int)(cur.u / Uh);
+  const long long r = cur.u - cur.hk * Uh;
+  if (excl <= r && r < excl + sum) {
+    long long x = excl;
+    int g = g0;
+    for (;; ++g) {
+      const int n = range_units(group_range(p, g / p.RT, g % p.RT));
+      if (r < x + n) break;
+      x += n;
+    }
+    s_g = g;
+    s_first = x;
+  }
+  __syncthreads();
+  cur.g = s_g;
+  cur.g_first = cur.hk * Uh + s_first;
+  return true;
+}
+
+// The next run of this CTA; false when there is none.  Uniform over the CTA.
+__device__ __forceinline__ bool cursor_next(const FwdParams &p, Cursor &cur, Run &run) {
+  if (cur.u >= cur.u1) return false;
+  for (;;) {
+    run.b = cur.g / p.RT;
+    run.rt = cur.g - run.b * p.RT;
+    run.range = group_range(p, run.b, run.rt);
+    run.n = range_units(run.range);
+    if (cur.u < cur.g_first + run.n) break;
+    cur.g_first += run.n;
+    if (++cur.g == p.NG) {
+      cur.g = 0;
+      ++cur.hk;
+    }
+  }
+  run.hk = cur.hk;
+  run.off = (int)(cur.u - cur.g_first);
+  const long long left = cur.u1 - cur.u;
+  run.cnt = (int)(run.n - run.off < left ? run.n - run.off : left);
+  run.slot = 2 * blockIdx.x + (cur.g_first > cur.u0 ? 1 : 0);
+  cur.u += run.cnt;
+  return true;
+}
+
+// Whether a row at position pos_q sees key pos (below the row tile's hi).
+__device__ __forceinline__ bool sees(const FwdParams &p, long long pos_q, int pos) {
+  if (p.causal && pos > pos_q) return false;
+  return p.window <= 0 || pos_q - pos < p.window;
+}
+
+// The logarithm (base 2) of a page's value scale, and its inverse; scales below 2^-60 count as 0.
+__device__ __forceinline__ float scale_log2(float vs, float *inv, bool *zero) {
+  *zero = !(vs >= kMinScale);
+  const float s = *zero ? kMinScale : vs;
+  const float lv = log2f(s);
+  *inv = exp2f(-lv);
+  return lv;
+}
+
+// A row's final factors from its reference M and sum l: O = O' * scale.  The extra softmax column
+// (sink or off-by-one) enters here, once.
+struct RowEnd {
+  float scale, lse;
+};
+__device__ __forceinline__ RowEnd row_end(const FwdParams &p, int h, float M, float l) {
+  RowEnd e;
+  float top = M;
+  if (p.sink || p.off_by_one) {
+    const float s2 = p.sink ? p.sink[h] * kLog2e : 0.f;
+    top = max_nan(M, s2);
+    l = (M == -CUDART_INF_F ? 0.f : l * exp2f(M - top)) + exp2f(s2 - top);
+    if (s2 == -CUDART_INF_F && M == -CUDART_INF_F) l = 0.f;
+  }
+  if (top == -CUDART_INF_F) {
+    e.scale = 0.f;
+    e.lse = -CUDART_INF_F;
+  } else {
+    e.scale = (M == -CUDART_INF_F ? 0.f : exp2f(M - top)) / l;
+    e.lse = kLn2 * (top + log2f(l));
+  }
+  return e;
+}
+
+// Where row r of an item lives in O (first element) and in LSE.
+__device__ __forceinline__ size_t o_row(const FwdParams &p, int b, int hk, int r) {
+  const int i = r / p.G, h = hk * p.G + (r - i * p.G);
+  return (((size_t)b * p.Sq + i) * p.Hq + h) * p.c.D;
+}
+__device__ __forceinline__ size_t lse_at(const FwdParams &p, int b, int hk, int r) {
+  const int i = r / p.G, h = hk * p.G + (r - i * p.G);
+  return ((size_t)b * p.Hq + h) * p.Sq + i;
+}
+__device__ __forceinline__ float *scores_row(const FwdParams &p, int b, int hk, int r) {
+  return p.scores + (((size_t)b * p.c.Hkv + hk) * p.R + r) * p.Lpad;
+}
+
+}  // namespace cache
+}  // namespace attn
