@@ -10,8 +10,6 @@
 namespace attn {
 namespace cache {
 
-int simt_row_tile();
-
 namespace {
 
 constexpr size_t kAlign = 256;
@@ -28,6 +26,7 @@ int log2_of(int x) {
 int validate(const attn_cache *c) {
   if (!c) return ATTN_ERR_INVALID;
   if (c->kind != ATTN_CACHE_E4M3 && c->kind != ATTN_CACHE_INT8) return ATTN_ERR_INVALID;
+  if ((long long)c->num_pages * c->Hkv > INT_MAX) return ATTN_ERR_UNSUPPORTED;  // TMA coordinates
   if (c->num_pages < 1 || c->Hkv < 1 || c->Hkv > 65535 || c->D < 16) return ATTN_ERR_INVALID;
   if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) return ATTN_ERR_UNSUPPORTED;
   if (c->D % 16 != 0 || c->D > 512) return ATTN_ERR_UNSUPPORTED;
@@ -96,6 +95,8 @@ int validate(const attn_cache *c, const attn_cache_seqs *s, const attn_cache_fwd
   return ATTN_OK;
 }
 
+bool use_mma(const attn_cache *c, const attn_cache_fwd_args *a) { return mma_supported(a->dtype, c->D); }
+
 struct FwdLayout {
   size_t prefix, o_part, ml_part, scores, total;
 };
@@ -108,12 +109,13 @@ FwdParams fwd_params(const attn_cache *c, const attn_cache_seqs *s, const attn_c
   p.Hq = a->Hq;
   p.G = a->Hq / c->Hkv;
   p.R = p.G * a->Sq;
-  p.row_tile = simt_row_tile();
+  const bool mma = use_mma(c, a);
+  p.row_tile = mma ? mma_row_tile(c->D, p.R) : simt_row_tile();
   p.RT = (p.R + p.row_tile - 1) / p.row_tile;
   p.NG = s->B * p.RT;
   const long long cap = (long long)s->max_pages * c->page_size;
   const long long most = std::max(1LL, (long long)p.NG * c->Hkv * ((cap + 31) / 32 * 32 + kUnit - 1) / kUnit);
-  p.max_ctas = (int)std::min(most, 4LL * device_sm_count());
+  p.max_ctas = (int)std::min(most, (mma ? mma_ctas_per_sm(c->D, p.row_tile) : 4LL) * device_sm_count());
   p.causal = a->causal ? 1 : 0;
   p.window = a->window > 0 ? a->window : 0;
   p.cap = a->softcap;
@@ -193,7 +195,7 @@ size_t attn_cache_fwd_workspace_size(const attn_cache *c, const attn_cache_seqs 
 
 const char *attn_cache_path_name(const attn_cache *c, const attn_cache_seqs *s, const attn_cache_fwd_args *a) {
   if (validate(c, s, a) != ATTN_OK) return "";
-  return "simt";
+  return use_mma(c, a) ? "mma" : "simt";
 }
 
 int attn_cache_fwd(const attn_cache *c, const attn_cache_seqs *s, const attn_cache_fwd_args *a, void *O,
@@ -213,7 +215,7 @@ int attn_cache_fwd(const attn_cache *c, const attn_cache_seqs *s, const attn_cac
   p.O = O;
   p.LSE = LSE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_fwd_simt(p, a->dtype, c->kind, st);
+  cudaError_t e = use_mma(c, a) ? launch_fwd_mma(p, c->kind, st) : launch_fwd_simt(p, a->dtype, c->kind, st);
   if (e == cudaSuccess) e = launch_fwd_join(p, a->dtype, st);
   if (e == cudaSuccess && a->weights && s->max_pages > 0) e = launch_weights(p, st);
   return cuda_status(e);

@@ -2,6 +2,7 @@
 // conversions, the scale rule, and the plan that spreads attention over the grid.
 #pragma once
 
+#include <cuda.h>  // CUtensorMap (type only)
 #include <cuda_fp16.h>
 #include <limits.h>
 #include <math_constants.h>
@@ -182,6 +183,15 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 cudaError_t launch_fwd_simt(const FwdParams &p, int dtype, int kind, cudaStream_t st);
+int simt_row_tile();
+
+// Tensor-core path.
+bool mma_supported(int dtype, int D);
+int mma_row_tile(int D, int R);
+int mma_ctas_per_sm(int D, int row_tile);
+cudaError_t launch_fwd_mma(const FwdParams &p, int kind, cudaStream_t st);
+bool make_tmap_codes(CUtensorMap *m, const void *base, int D, int page, long long heads, int box_rows);
+
 cudaError_t launch_fwd_join(const FwdParams &p, int dtype, cudaStream_t st);
 cudaError_t launch_weights(const FwdParams &p, cudaStream_t st);
 

@@ -1,0 +1,658 @@
+// cache_fwd_mma.cu -- attention over the 8-bit cache on the tensor cores: bf16 queries, head dims 64,
+// 128 and 256.
+//
+// Decoding reads 2 D bytes of codes per key and kv head and does 4 D flops per byte and query row, so
+// with the few rows of a step (G heads share a kv head) it is bound by memory; what can keep it from
+// that is the work per byte: widening codes, loads from shared memory, softmax.  Hence:
+//   - Each warp works alone.  It owns a ring of slices (SK keys of K and V), lane 0 fills it by TMA
+//     (the table's page ids and the scales of 32 slices ahead sit one per lane in registers), and no
+//     warp waits for another until a run of units ends.
+//   - Codes go from shared memory to registers 16 at a time in the order in which the MMA wants its B
+//     operand, whatever that does to the order of d (both products are free to permute what they sum
+//     over, and Q is laid out to match), and are widened there to fp16, exactly; no shuffles, no second
+//     copy.  m16n8k16 with fp16 operands: rows of Q (or P) as A, 8 keys (or 8 columns of V) as B.
+//   - TMA's swizzle makes both 16-byte access patterns free of bank conflicts.
+//   - Q is scaled per row by a power of two into fp16's range: exact for elements within 2^-31 of the
+//     row's largest.
+//   - P is rounded to fp16 (half a step: 2^-11 of each probability, eight times finer than the bf16 result).
+#include "cache_work.cuh"
+#include "tc_common.cuh"
+
+namespace attn {
+namespace cache {
+namespace {
+
+using namespace attn::tc;
+
+constexpr int kWarps = kThreads / 32;
+constexpr float kZeroLog = kMinScaleExp - 1, kZeroInv = 2.f / kMinScale;
+
+template <int D_, int MT_>
+struct Cfg {
+  static constexpr int D = D_, MT = MT_;
+  static constexpr int SK = D == 256 ? 16 : 32;        // keys of a slice
+  static constexpr int NH = SK / 16;                   // 16-key halves: each lies in one page
+  static constexpr int BLK = D < 128 ? D : 128;        // columns of one TMA box row
+  static constexpr int NB = D / BLK;                   // boxes per row
+  static constexpr int CH = BLK / 64;                  // 16-byte chunks per lane and key for Q K^T
+  static constexpr int KS = D / 16;                    // k-steps of Q K^T
+  static constexpr int NT = D / 8;                     // n-tiles of P V
+  static constexpr int STAGE = 2 * SK * D;             // bytes of a slice, K then V
+  static constexpr int DEPTH = D == 64 ? (MT == 1 ? 3 : 4) : 2;
+  static constexpr int CTAS = MT == 1 ? (D == 64 ? 4 : D == 128 ? 3 : 2) : 2;
+  static constexpr bool QREG = D * MT <= 128;          // Q fragments in registers, else in shared memory
+  static constexpr int ROWS = 16 * MT;
+  static constexpr int OPITCH = D + 4;
+  static constexpr size_t RING = (size_t)kWarps * DEPTH * STAGE;
+  static constexpr size_t O_BYTES = (size_t)ROWS * OPITCH * 4;
+  static constexpr size_t Q_BYTES = QREG ? 0 : (size_t)MT * KS * 32 * 16;
+  static constexpr size_t SMEM = 1024 + RING + O_BYTES + Q_BYTES + kWarps * ROWS * 8 + kWarps * DEPTH * 8;
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_f16(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+  return v;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Four codes of a word widened to two fp16 pairs, exactly.  int8: code + 128 under the bits of 1024
+// is 1152 + code in fp16.
+template <int KIND> __device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  if (KIND == ATTN_CACHE_E4M3) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(w));
+  } else {
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    __half2 x = __hsub2(*reinterpret_cast<__half2 *>(&a), bias), y = __hsub2(*reinterpret_cast<__half2 *>(&b), bias);
+    lo = *reinterpret_cast<uint32_t *>(&x);
+    hi = *reinterpret_cast<uint32_t *>(&y);
+  }
+}
+
+// NaNs of an fp16 pair: *bad has 1.0 in their places, the result 0.
+__device__ __forceinline__ uint32_t split_nan(uint32_t h, uint32_t *bad) {
+  const uint32_t lo = (h & 0x7fffu) > 0x7c00u, hi = (h & 0x7fff0000u) > 0x7c000000u;
+  *bad = (lo ? 0x3c00u : 0u) | (hi ? 0x3c000000u : 0u);
+  return (lo ? 0u : h & 0xffffu) | (hi ? 0u : h & 0xffff0000u);
+}
+
+// cap * tanh(u / cap) * log2(e) with y = 2 log2(e) u / cap: 1 - 2 / (1 + 2^y).  Absolute error some
+// steps of the cap; saturates cleanly (2^y = inf gives 1, 0 gives -1).
+__device__ __forceinline__ float softcap_log2(float y, float cap_log2) {
+  return cap_log2 - __fdividef(2.f * cap_log2, 1.f + ex2(y));
+}
+
+// Byte offset of 16-byte chunk `ch` of key row `row` in a box, under TMA's swizzle.
+template <int BLK> __device__ __forceinline__ uint32_t swz(int row, int ch) {
+  if (BLK == 128) return row * 128 + ((ch ^ (row & 7)) << 4);
+  return row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
+}
+
+template <int KIND, int D, int MT>
+__global__ void __launch_bounds__(kThreads, (Cfg<D, MT>::CTAS))
+cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap) {
+  using C = Cfg<D, MT>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), ring0 = (raw + 1023u) & ~1023u;
+  uint8_t *base = smem_raw + (ring0 - raw);
+  float *s_o = reinterpret_cast<float *>(base + C::RING);                                // [ROWS][OPITCH]
+  uint4 *s_q = reinterpret_cast<uint4 *>(base + C::RING + C::O_BYTES);                   // [MT][KS][32]
+  float2 *s_ml = reinterpret_cast<float2 *>(base + C::RING + C::O_BYTES + C::Q_BYTES);   // [kWarps][ROWS]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const uint32_t ring = ring0 + warp * (C::DEPTH * C::STAGE);
+  const uint32_t bars = ring0 + C::RING + C::O_BYTES + C::Q_BYTES + kWarps * C::ROWS * 8 + warp * (C::DEPTH * 8);
+  if (lane == 0) {
+#pragma unroll
+    for (int s = 0; s < C::DEPTH; ++s) mbar_init(bars + 8 * s, 1);
+    fence_barrier_init();
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+  }
+  __syncwarp();
+
+  Cursor cur;
+  if (!cursor_begin(p, cur)) return;
+  Run run;
+  uint32_t phases = 0;  // parity of each stage's next completion
+  int stage = 0;
+  bool dead = false;    // a wait gave up: recorded; this warp computes no further
+  const float cap_log2 = p.cap * kLog2e;
+  while (cursor_next(p, cur, run)) {
+    const int r0 = run.rt * C::ROWS, rows = min(C::ROWS, p.R - r0);
+    const int key0 = run.range.lo + run.off * kUnit, key1 = min(run.range.hi, key0 + run.cnt * kUnit);
+    // This warp's slices: key0 + (warp + 4 x) SK for x < n_slices.
+    const int n_slices = (key1 - key0 - warp * C::SK + kWarps * C::SK - 1) / (kWarps * C::SK);  // <= 0: none
+
+    // Page ids and scales of 32 slices, one per lane: `now` of the batch being consumed, `nxt` of the
+    // following one.
+    int nxt_id[C::NH], id_now[C::NH];
+    float ks_now[C::NH], lv_now[C::NH], inv_now[C::NH], ks_nxt[C::NH], lv_nxt[C::NH], inv_nxt[C::NH];
+    auto load_ids = [&](int batch, int *ids) {
+      const int x = batch * 32 + lane;
+#pragma unroll
+      for (int h = 0; h < C::NH; ++h) {
+        const int pos = key0 + (warp + kWarps * x) * C::SK + 16 * h;
+        ids[h] = x < n_slices && pos < key1 ? page_of(p.c, run.b, pos) : -1;
+      }
+    };
+    // (A value scale that counts as 0 has kZeroLog for its logarithm.)
+    auto load_scales = [&](const int *ids, float *ks, float *lv, float *inv) {
+#pragma unroll
+      for (int h = 0; h < C::NH; ++h) {
+        ks[h] = 0.f;
+        float vs = 1.f;
+        if (ids[h] >= 0) {
+          const size_t at = (size_t)ids[h] * p.c.Hkv + run.hk;
+          ks[h] = p.c.k_scale[at];
+          vs = p.c.v_scale[at];
+        }
+        bool zero;
+        lv[h] = scale_log2(vs, &inv[h], &zero);
+        if (zero) {  // any reference does for values of 0, if the sum undoes it
+          lv[h] = kZeroLog;
+          inv[h] = kZeroInv;
+        }
+      }
+    };
+    // Fills ring stage `st` with slice x (ids: its batch).  All lanes call it; lane 0 issues.
+    auto issue = [&](int x, int st, const int *ids) {
+      const uint32_t bar = bars + 8 * st, dst = ring + st * C::STAGE;
+      int id[C::NH];
+#pragma unroll
+      for (int h = 0; h < C::NH; ++h) id[h] = __shfl_sync(~0u, ids[h], x & 31);
+      if (lane == 0) {
+        const int pos = key0 + (warp + kWarps * x) * C::SK, slot = pos & (p.c.page - 1);
+        const bool two = C::NH == 2 && p.c.page == 16;  // the halves are pages of their own
+        uint32_t bytes = 0;
+        if (!two) bytes = id[0] >= 0 ? C::STAGE : 0;
+        else bytes = (id[0] >= 0 ? C::STAGE / 2 : 0) + (id[C::NH - 1] >= 0 ? C::STAGE / 2 : 0);
+        mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+        for (int h = 0; h < C::NH; ++h) {
+          if (h > 0 && !two) break;
+          if (id[h] < 0) continue;
+          const int head = id[h] * p.c.Hkv + run.hk;
+#pragma unroll
+          for (int j = 0; j < C::NB; ++j) {
+            const uint32_t to = dst + j * (C::SK * C::BLK) + h * (16 * C::BLK);
+            tma_load_3d(to, &kmap, bar, j * C::BLK, slot, head);
+            tma_load_3d(to + C::SK * D, &vmap, bar, j * C::BLK, slot, head);
+          }
+        }
+      }
+    };
+
+    load_ids(0, id_now);
+#pragma unroll
+    for (int s = 0; s < C::DEPTH; ++s)
+      if (s < n_slices) {
+        int st = stage + s;
+        issue(s, st >= C::DEPTH ? st - C::DEPTH : st, id_now);
+      }
+    load_scales(id_now, ks_now, lv_now, inv_now);
+#pragma unroll
+    for (int h = 0; h < C::NH; ++h) nxt_id[h] = -1, ks_nxt[h] = 0.f, lv_nxt[h] = 0.f, inv_nxt[h] = 1.f;
+    if (n_slices > 32) load_ids(1, nxt_id);
+
+    // Queries: rows g and g + 8 of each 16, this lane's columns, scaled into fp16.
+    uint32_t qf[C::QREG ? MT : 1][C::QREG ? C::KS : 1][4];
+    float q_mul[MT][2];  // what undoes the scaling, times the softmax scale (and log2 e without a cap)
+    long long pos_q[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      uint4 raw_q[2][D / 32];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int r = r0 + mt * 16 + 8 * y + g;
+        const int i = r / p.G, h = run.hk * p.G + (r - i * p.G);
+        pos_q[mt][y] = (long long)run.range.len - p.Sq + i;
+        float amax = 0.f;
+#pragma unroll
+        for (int j = 0; j < C::NB; ++j)
+#pragma unroll
+          for (int x = 0; x < C::BLK / 32; ++x) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (r < p.R)
+              u = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + run.b * p.q_sb + i * p.q_ss +
+                                                   h * p.q_sh + j * C::BLK + t * (C::BLK / 4) + x * 8);
+            raw_q[y][j * (C::BLK / 32) + x] = u;
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              amax = max_nan(amax, max_nan(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+          }
+        amax = max_nan(amax, __shfl_xor_sync(~0u, amax, 1));
+        amax = max_nan(amax, __shfl_xor_sync(~0u, amax, 2));
+        // 2^x that brings the largest element into [2^14, 2^15); 1 for rows that are 0 or not finite.
+        int x = 14 - ((int)(__float_as_uint(amax) >> 23) - 127);
+        if (!(amax > 0.f) || !(amax <= 3.402823466e38f)) x = 0;
+        x = x > 126 ? 126 : x;
+        const float up = __uint_as_float((unsigned)(x + 127) << 23);
+        q_mul[mt][y] = __uint_as_float((unsigned)(127 - x) << 23) * p.scale * (p.cap > 0.f ? 2.f * kLog2e * p.inv_cap : kLog2e);
+#pragma unroll
+        for (int z = 0; z < D / 32; ++z) {
+          uint4 &u = raw_q[y][z];
+          uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack_h2(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xffff0000u) * up);
+          u = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      // A fragment of k-step s: columns 4 s .. 4 s + 3 of this lane's (words 2 s and 2 s + 1).
+#pragma unroll
+      for (int s = 0; s < C::KS; ++s) {
+        const uint4 &u = raw_q[0][s / 2], &v = raw_q[1][s / 2];
+        const uint4 f = s % 2 ? make_uint4(u.z, v.z, u.w, v.w) : make_uint4(u.x, v.x, u.y, v.y);
+        if (C::QREG) {
+          qf[C::QREG ? mt : 0][C::QREG ? s : 0][0] = f.x;
+          qf[C::QREG ? mt : 0][C::QREG ? s : 0][1] = f.y;
+          qf[C::QREG ? mt : 0][C::QREG ? s : 0][2] = f.z;
+          qf[C::QREG ? mt : 0][C::QREG ? s : 0][3] = f.w;
+        } else if (warp == 0) {
+          s_q[(mt * C::KS + s) * 32 + lane] = f;
+        }
+      }
+    }
+    if (!C::QREG) __syncthreads();  // (the previous run's reads of s_q ended before its own barriers)
+
+    float m[MT][2], l[MT][2], o[MT][C::NT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        m[mt][y] = -CUDART_INF_F;
+        l[mt][y] = 0.f;
+      }
+#pragma unroll
+      for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[mt][n][x] = 0.f;
+    }
+    // Positions between which every row of the tile sees a key (rows' positions ascend).
+    const long long first_q = (long long)run.range.len - p.Sq + r0 / p.G, last_q = (long long)run.range.len - p.Sq + (r0 + rows - 1) / p.G;
+    const long long all_below = p.causal ? min((long long)run.range.hi, first_q + 1) : run.range.hi;
+    const long long all_from = p.window > 0 ? last_q - p.window + 1 : 0;
+
+    for (int x = 0; x < n_slices; ++x) {
+      const int pos = key0 + (warp + kWarps * x) * C::SK;
+      if (x > 0 && (x & 31) == 0) {
+#pragma unroll
+        for (int h = 0; h < C::NH; ++h) {
+          id_now[h] = nxt_id[h];
+          ks_now[h] = ks_nxt[h];
+          lv_now[h] = lv_nxt[h];
+          inv_now[h] = inv_nxt[h];
+        }
+        if (n_slices > (x | 31) + 1) load_ids((x >> 5) + 1, nxt_id);
+      }
+      // This slice's scales.
+      float ks[C::NH], lv[C::NH], inv[C::NH];
+      bool zero[C::NH], bad = false, gone[C::NH];
+#pragma unroll
+      for (int h = 0; h < C::NH; ++h) {
+        ks[h] = __shfl_sync(~0u, ks_now[h], x & 31);
+        lv[h] = __shfl_sync(~0u, lv_now[h], x & 31);
+        inv[h] = __shfl_sync(~0u, inv_now[h], x & 31);
+        zero[h] = lv[h] == kZeroLog;
+        gone[h] = __shfl_sync(~0u, id_now[h], x & 31) < 0;
+        bad |= gone[h] | zero[h];
+      }
+      const bool partial = bad || pos + C::SK > all_below || pos < all_from;
+      const uint32_t sk = ring + stage * C::STAGE, sv = sk + C::SK * D;
+      if (!dead) dead = !__all_sync(~0u, mbar_wait(bars + 8 * stage, (phases >> stage) & 1u, p.c.status));
+      phases ^= 1u << stage;
+      if (!dead) {
+        float s[MT][C::SK / 8][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int n = 0; n < C::SK / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
+        // Scores: n-tile n holds keys 8 n .. 8 n + 7, key 8 n + g on the lanes of group g.
+#pragma unroll
+        for (int j = 0; j < C::NB; ++j)
+#pragma unroll
+          for (int c = 0; c < C::CH; ++c) {
+            uint4 kw[C::SK / 8];
+#pragma unroll
+            for (int n = 0; n < C::SK / 8; ++n)
+              kw[n] = lds128(sk + j * (C::SK * C::BLK) + swz<C::BLK>(8 * n + g, t * C::CH + c));
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int step = (j * C::CH + c) * 4 + w;
+              uint4 qs[MT];
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+                if (!C::QREG) qs[mt] = s_q[(mt * C::KS + step) * 32 + lane];
+#pragma unroll
+              for (int n = 0; n < C::SK / 8; ++n) {
+                const uint32_t word = w == 0 ? kw[n].x : w == 1 ? kw[n].y : w == 2 ? kw[n].z : kw[n].w;
+                uint32_t b0, b1;
+                widen4<KIND>(word, b0, b1);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                  if (C::QREG) {
+                    mma_f16(s[mt][n], qf[C::QREG ? mt : 0][C::QREG ? step : 0], b0, b1);
+                  } else {
+                    const uint32_t a[4] = {qs[mt].x, qs[mt].y, qs[mt].z, qs[mt].w};
+                    mma_f16(s[mt][n], a, b0, b1);
+                  }
+                }
+              }
+            }
+          }
+        // Softmax: logits in base 2, masked, with the values' scale in the exponent.
+        uint32_t pf[MT][C::NH][4];
+        bool moved = false;
+        float mn[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float top = m[mt][y];
+#pragma unroll
+            for (int n = 0; n < C::SK / 8; ++n) {
+              const float f = q_mul[mt][y] * ks[n / 2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float v = s[mt][n][2 * y + e] * f;
+                if (p.cap > 0.f) v = softcap_log2(v, cap_log2);
+                if (partial) {
+                  const int key = pos + 8 * n + 2 * t + e;
+                  if (gone[n / 2] || key >= key1 || !sees(p, pos_q[mt][y], key)) v = -CUDART_INF_F;
+                }
+                s[mt][n][2 * y + e] = v;
+              }
+              if (p.scores) {
+                const int r = mt * 16 + 8 * y + g;
+                if (r < rows)
+                  *reinterpret_cast<float2 *>(scores_row(p, run.b, run.hk, r0 + r) + pos + 8 * n + 2 * t) =
+                      make_float2(s[mt][n][2 * y], s[mt][n][2 * y + 1]);
+              }
+              s[mt][n][2 * y] += lv[n / 2];
+              s[mt][n][2 * y + 1] += lv[n / 2];
+              top = max_nan(top, max_nan(s[mt][n][2 * y], s[mt][n][2 * y + 1]));
+            }
+            top = max_nan(top, __shfl_xor_sync(~0u, top, 1));
+            top = max_nan(top, __shfl_xor_sync(~0u, top, 2));
+            mn[mt][y] = top;
+            moved |= top != m[mt][y];
+          }
+        }
+        if (__any_sync(~0u, moved)) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const float a = mn[mt][y] == -CUDART_INF_F ? 1.f : ex2(m[mt][y] - mn[mt][y]);
+              m[mt][y] = mn[mt][y];
+              l[mt][y] *= a;
+#pragma unroll
+              for (int n = 0; n < C::NT; ++n) {
+                o[mt][n][2 * y] *= a;
+                o[mt][n][2 * y + 1] *= a;
+              }
+            }
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int h = 0; h < C::NH; ++h)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int y = q & 1, n = 2 * h + (q >> 1);
+              const float ref = m[mt][y] == -CUDART_INF_F ? 0.f : m[mt][y];
+              const float e0 = ex2(s[mt][n][2 * y] - ref), e1 = ex2(s[mt][n][2 * y + 1] - ref);
+              l[mt][y] += (e0 + e1) * inv[h];
+              pf[mt][h][q] = zero[h] ? 0u : pack_h2(e0, e1);
+            }
+        // O += P V: lane t has keys 2t, 2t + 1, 2t + 8, 2t + 9 of each 16 as the B operand's rows, and
+        // BLK / 8 neighbouring columns, one for each n-tile.
+#pragma unroll
+        for (int j = 0; j < C::NB; ++j)
+#pragma unroll
+          for (int h = 0; h < C::NH; ++h) {
+            uint32_t vw[4][C::BLK / 32];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int key = 16 * h + 2 * t + (q & 1) + 8 * (q >> 1);
+              const uint32_t at = sv + j * (C::SK * C::BLK);
+              if (C::BLK == 128) {
+                const uint4 u = lds128(at + swz<C::BLK>(key, g));
+                vw[q][0] = u.x;
+                vw[q][1] = u.y;
+                vw[q][C::BLK / 32 - 2] = u.z;
+                vw[q][C::BLK / 32 - 1] = u.w;
+              } else {
+                const uint2 u = lds64(at + swz<C::BLK>(key, g >> 1) + (g & 1) * 8);
+                vw[q][0] = u.x;
+                vw[q][1] = u.y;
+              }
+              // Slots that hold no token of the sequence may hold anything.
+              if (partial && (gone[h] || zero[h] || pos + key >= key1)) {
+#pragma unroll
+                for (int w = 0; w < C::BLK / 32; ++w) vw[q][w] = 0u;
+              }
+            }
+#pragma unroll
+            for (int w = 0; w < C::BLK / 32; ++w)
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const uint32_t sel = z ? 0x7362 : 0x5140;
+                uint32_t b0[2], b1[2];
+                widen4<KIND>(__byte_perm(vw[0][w], vw[1][w], sel), b0[0], b0[1]);
+                widen4<KIND>(__byte_perm(vw[2][w], vw[3][w], sel), b1[0], b1[1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int n = j * (C::BLK / 8) + 4 * w + 2 * z + e;
+                  if (KIND == ATTN_CACHE_E4M3 && partial) {
+                    // A NaN value reaches the rows that see its key, and no other: its place counts as 0
+                    // in the product, and a product of what rows see with where NaNs are tells them.
+                    uint32_t n0, n1;
+                    const uint32_t c0 = split_nan(b0[e], &n0), c1 = split_nan(b1[e], &n1);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                      uint32_t see[4];
+#pragma unroll
+                      for (int q = 0; q < 4; ++q) {
+                        const int k0 = pos + 16 * h + 2 * t + 8 * (q >> 1);
+                        see[q] = (k0 < key1 && sees(p, pos_q[mt][q & 1], k0) ? 0x3c00u : 0u) |
+                                 (k0 + 1 < key1 && sees(p, pos_q[mt][q & 1], k0 + 1) ? 0x3c000000u : 0u);
+                      }
+                      float hit[4] = {0.f, 0.f, 0.f, 0.f};
+                      mma_f16(hit, see, n0, n1);
+                      mma_f16(o[mt][n], pf[mt][h], c0, c1);
+#pragma unroll
+                      for (int q = 0; q < 4; ++q)
+                        if (hit[q] > 0.f) o[mt][n][q] = CUDART_NAN_F;
+                    }
+                  } else {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) mma_f16(o[mt][n], pf[mt][h], b0[e], b1[e]);
+                  }
+                }
+              }
+          }
+      }
+      __syncwarp();  // every lane has read the stage
+      if (x + C::DEPTH < n_slices && !dead) {
+        const int y = x + C::DEPTH;
+        if ((y & 31) == 0) load_scales(nxt_id, ks_nxt, lv_nxt, inv_nxt);
+        issue(y, stage, (y >> 5) == (x >> 5) ? id_now : nxt_id);
+      }
+      stage = stage + 1 == C::DEPTH ? 0 : stage + 1;
+    }
+
+    // The four warps' rows joined in shared memory, and the run's end.
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float v = l[mt][y];
+        v += __shfl_xor_sync(~0u, v, 1);
+        v += __shfl_xor_sync(~0u, v, 2);
+        if (dead) v = CUDART_NAN_F;
+        if (t == 0) s_ml[warp * C::ROWS + mt * 16 + 8 * y + g] = make_float2(m[mt][y], v);
+      }
+    __syncthreads();
+    float f[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float M = -CUDART_INF_F;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = max_nan(M, s_ml[w * C::ROWS + mt * 16 + 8 * y + g].x);
+        f[mt][y] = m[mt][y] == -CUDART_INF_F ? 0.f : ex2(m[mt][y] - M);
+      }
+    for (int w = 0; w < kWarps; ++w) {
+      if (warp == w) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int n = 0; n < C::NT; n += 4) {
+                // n-tile n of a block: column (BLK / 8) (2 t + e) + n.
+                const int j = n / (C::BLK / 8), d = j * C::BLK + (C::BLK / 8) * (2 * t + e) + n % (C::BLK / 8);
+                float4 *at = reinterpret_cast<float4 *>(s_o + (mt * 16 + 8 * y + g) * C::OPITCH + d);
+                float4 v = w ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
+                if (f[mt][y] != 0.f) {
+                  v.x += f[mt][y] * o[mt][n][2 * y + e];
+                  v.y += f[mt][y] * o[mt][n + 1][2 * y + e];
+                  v.z += f[mt][y] * o[mt][n + 2][2 * y + e];
+                  v.w += f[mt][y] * o[mt][n + 3][2 * y + e];
+                }
+                *at = v;
+              }
+      }
+      __syncthreads();
+    }
+    const bool whole = run.cnt == run.n;
+    for (int r = warp; r < rows; r += kWarps) {
+      float M = -CUDART_INF_F, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = max_nan(M, s_ml[w * C::ROWS + r].x);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 ml = s_ml[w * C::ROWS + r];
+        if (ml.x != -CUDART_INF_F) L += ml.y * ex2(ml.x - M);
+      }
+      float scale = 1.f;
+      if (whole) {
+        const RowEnd e = row_end(p, run.hk * p.G + (r0 + r) % p.G, M, L);
+        scale = e.scale;
+        if (lane == 0) p.LSE[lse_at(p, run.b, run.hk, r0 + r)] = e.lse;
+      } else if (lane == 0) {
+        p.ml_part[(size_t)run.slot * C::ROWS + r] = make_float2(M, L);
+      }
+      for (int d = lane * 4; d < D; d += 128) {
+        float4 v = *reinterpret_cast<const float4 *>(s_o + r * C::OPITCH + d);
+        if (whole) {
+          if (M == -CUDART_INF_F) v = make_float4(0.f, 0.f, 0.f, 0.f);
+          uint2 u;
+          __nv_bfloat162 a = __floats2bfloat162_rn(v.x * scale, v.y * scale), b = __floats2bfloat162_rn(v.z * scale, v.w * scale);
+          u.x = *reinterpret_cast<uint32_t *>(&a);
+          u.y = *reinterpret_cast<uint32_t *>(&b);
+          *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.O) + o_row(p, run.b, run.hk, r0 + r) + d) = u;
+        } else {
+          *reinterpret_cast<float4 *>(p.o_part + ((size_t)run.slot * C::ROWS + r) * D + d) = v;
+        }
+      }
+    }
+    __syncthreads();  // s_o and s_ml are free for the next run
+  }
+}
+
+// The kernel's shared-memory limit, raised once per device.
+template <typename K> cudaError_t raise_smem(K kernel, std::atomic<unsigned long long> &done, size_t bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+template <int KIND, int D, int MT>
+cudaError_t launch_t(const FwdParams &p, cudaStream_t st) {
+  using C = Cfg<D, MT>;
+  auto kernel = cache_fwd_mma_kernel<KIND, D, MT>;
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = raise_smem(kernel, done, C::SMEM);
+  if (e != cudaSuccess) return e;
+  CUtensorMap km, vm;
+  const int rows = p.c.page < C::SK ? p.c.page : C::SK;
+  if (!make_tmap_codes(&km, p.c.k, D, p.c.page, (long long)p.c.num_pages * p.c.Hkv, rows) ||
+      !make_tmap_codes(&vm, p.c.v, D, p.c.page, (long long)p.c.num_pages * p.c.Hkv, rows))
+    return cudaErrorInvalidValue;
+  kernel<<<p.max_ctas, kThreads, C::SMEM, st>>>(p, km, vm);
+  return counted(cudaGetLastError());
+}
+
+template <int KIND> cudaError_t launch_k(const FwdParams &p, cudaStream_t st) {
+  const bool two = p.row_tile == 32;
+  switch (p.c.D) {
+    case 64: return two ? launch_t<KIND, 64, 2>(p, st) : launch_t<KIND, 64, 1>(p, st);
+    case 128: return two ? launch_t<KIND, 128, 2>(p, st) : launch_t<KIND, 128, 1>(p, st);
+    default: return launch_t<KIND, 256, 1>(p, st);
+  }
+}
+
+}  // namespace
+
+bool mma_supported(int dtype, int D) { return dtype == kBF16 && (D == 64 || D == 128 || D == 256); }
+
+// Rows of a work item: 16, or 32 where there are more rows than that and the accumulators fit
+// (head dims up to 128), so that widening a code serves two row tiles.
+int mma_row_tile(int D, int R) { return R > 16 && D <= 128 ? 32 : 16; }
+
+int mma_ctas_per_sm(int D, int row_tile) {
+  return row_tile == 32 ? 2 : D == 64 ? Cfg<64, 1>::CTAS : D == 128 ? Cfg<128, 1>::CTAS : Cfg<256, 1>::CTAS;
+}
+
+cudaError_t launch_fwd_mma(const FwdParams &p, int kind, cudaStream_t st) {
+  return kind == ATTN_CACHE_E4M3 ? launch_k<ATTN_CACHE_E4M3>(p, st) : launch_k<ATTN_CACHE_INT8>(p, st);
+}
+
+}  // namespace cache
+}  // namespace attn

@@ -1,0 +1,42 @@
+// cache_tmap.cu -- TMA maps over a cache's codes, encoded through the driver's entry point (resolved at
+// run time, so that the library loads without a driver).
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "cache_common.cuh"
+
+namespace attn {
+namespace cache {
+
+namespace {
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+}  // namespace
+
+// [pages * heads, page, D] codes in boxes of box_rows rows by at most 128 columns, swizzled over the box
+// row's width (128 bytes, or 64 for D = 64).
+bool make_tmap_codes(CUtensorMap *m, const void *base, int D, int page, long long heads, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)page, (cuuint64_t)heads};
+  cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)D * page};
+  cuuint32_t box[3] = {(cuuint32_t)(D < 128 ? D : 128), (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace cache
+}  // namespace attn

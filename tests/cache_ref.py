@@ -42,9 +42,19 @@ def gather(x, table_row, n, page):
     return x[ids].transpose(1, 2).reshape(-1, x.shape[1], x.shape[3])[:n]
 
 
-def attend(q, kv, vv, *, causal=False, window=0, softcap=0.0, sink=None, off_by_one=False, scale=None, hidden=None):
+def gather_scale(s, table_row, n, page):
+    """[n, H] scales of a sequence's tokens from [P, H]."""
+    return s[table_row[: -(-n // page)].long()].double().repeat_interleave(page, 0)[:n]
+
+
+def attend(q, kv, vv, *, causal=False, window=0, softcap=0.0, sink=None, off_by_one=False, scale=None, hidden=None, vs=None):
     """One sequence: q [Sq, Hq, D], kv / vv [n, Hkv, D] float64.  Returns O, LSE [Hq, Sq], weights [Hkv, n], and for the
-    error bounds sum p |v| [Sq, Hq, D] and the largest sum |q k| * scale."""
+    error bounds sum p |v| [Sq, Hq, D] and the largest sum |q k| * scale.
+
+    vs: the values' scales [n, Hkv], for the kernel that rounds its probabilities to fp16.  It rounds p_j vs_j / X with X =
+    max_j p_j vs_j (the reference that its exponents subtract is that maximum, or a smaller running one), and multiplies
+    v_j / vs_j: where the quotient is below 2^-14, fp16 is subnormal and half a step is 2^-25, not 2^-11 of it.  That adds
+    at most 2^-25 X sum_j |v_j| / vs_j to an output; it is returned with sum p |v|, in units of 2^-11."""
     Sq, Hq, D = q.shape
     n, Hkv, _ = kv.shape
     G = Hq // Hkv
@@ -76,6 +86,11 @@ def attend(q, kv, vv, *, causal=False, window=0, softcap=0.0, sink=None, off_by_
     clean = torch.where(see.any(0)[:, None, None], vx, 0.0)   # an unseen value may be NaN
     o = torch.einsum("hij,jhd->ihd", p, clean)
     pv = torch.einsum("hij,jhd->ihd", p, clean.abs())
+    if vs is not None and n:
+        sx = vs.repeat_interleave(G, 1)                                                    # [n, Hq]
+        X = (p * sx.T[:, None, :]).amax(2)                                                 # [Hq, Sq]
+        units = (clean.abs() / sx[..., None].clamp(min=2.0 ** -60)).sum(0)                 # [Hq, D]
+        pv = pv + 2.0 ** (-25 + 11) * torch.einsum("hi,hd->ihd", X, units)
     w = p.sum(1).view(Hkv, G, n).sum(1)
     return o, lse, w, pv, mag
 
@@ -89,8 +104,7 @@ def bounds(D, n, mag, softcap, half):
     the cap's tanh by some steps of the cap (8).  Tensor cores may truncate where others round: twice the first term.
     Probabilities: exp2 of a logit off by e is off by e (relative), in the sum above and in the one below: 2 e; exp2
     itself and the rescalings are off by some steps each (16); the sums of n float32 terms by n half steps each; a
-    probability rounded to fp16 (half=True) by 2^-11, its half step, and by 2^-24 of the largest where that is
-    subnormal (n of them)."""
+    probability rounded to fp16 (half=True) by 2^-11, its half step (attend's vs has what subnormal ones add)."""
     e = (2 * D + 4) * 2.0 ** -24 * mag + 8 * 2.0 ** -24 * softcap
     rel = 2 * e + 16 * 2.0 ** -24 + 2 * n * 2.0 ** -24
     if half:

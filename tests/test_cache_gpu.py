@@ -69,7 +69,8 @@ class Case:
             hid = None if hidden is None else hidden[b]
             if hid is not None:
                 kk, vv = torch.where(hid[:, None, None], 0.0, kk), torch.where(hid[:, None, None], 0.0, vv)
-            o, lse, w, pv, mag = ref.attend(self.q[b].double(), kk, vv, sink=self.sink if sink else None, hidden=hid, **kw)
+            vs = ref.gather_scale(self.vs, self.table[b], n, self.page) if half else None
+            o, lse, w, pv, mag = ref.attend(self.q[b].double(), kk, vv, sink=self.sink if sink else None, hidden=hid, vs=vs, **kw)
             e, rel = ref.bounds(self.D, n, mag, kw.get("softcap", 0.0), half)
             store = torch.finfo(self.q.dtype).eps / 2
             lim = store * o.abs() + (1 + store) * rel * pv + 2.0 ** -24 * pv + 1e-37
@@ -97,6 +98,8 @@ ODD = [1, 777, 0, 64, 65, 31, 130]
 def test_single_tokens(dtype, D, page, kind):
     c = Case(ODD, D=D, page=page, kind=kind, dtype=dtype, seed=D + page)
     c.check(*c.run())
+    path = fa().attn_cache_path_name(c.cuda["q"], c.cache, c.cuda["table"], c.cuda["lengths"])
+    assert path == ("mma" if dtype == BF16 and D in (64, 128, 256) else "simt")
 
 
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 1), (5, 5), (16, 2), (20, 2), (32, 1), (40, 1), (64, 8), (96, 3)])
@@ -349,7 +352,8 @@ def test_codes_past_32_bits():
         kf, vf = (ref.values(c[ids].cpu(), s[ids].cpu()) for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
         row = torch.arange(4)
         kk, vv = ref.gather(kf, row, 450, page), ref.gather(vf, row, 450, page)
-        o, lse, _, pv, mag = ref.attend(q[0].to(dtype).double(), kk, vv)
+        vs = ref.gather_scale(cache.v_scale[ids].cpu(), row, 450, page) if dtype == BF16 else None
+        o, lse, _, pv, mag = ref.attend(q[0].to(dtype).double(), kk, vv, vs=vs)
         _, rel = ref.bounds(D, 450, mag, 0.0, dtype == BF16)
         eps = torch.finfo(dtype).eps / 2
         assert ((O[0].cpu().double() - o).abs() <= eps * o.abs() + (1 + eps) * rel * pv).all()
@@ -622,7 +626,8 @@ def test_a_serving_loop(kind, dtype, D, page, window, softcap):
             L = int(n2[b])
             kk, vv = (ref.gather(ref.values(c.cpu(), s.cpu()), table[b].cpu(), L, page)
                       for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
-            o, lse, ww, pv, mag = ref.attend(q[b].double(), kk, vv, causal=True, window=window, softcap=softcap, sink=sink)
+            vs = ref.gather_scale(cache.v_scale.cpu(), table[b].cpu(), L, page) if dtype == BF16 else None
+            o, lse, ww, pv, mag = ref.attend(q[b].double(), kk, vv, causal=True, window=window, softcap=softcap, sink=sink, vs=vs)
             _, rel = ref.bounds(D, L, mag, softcap, dtype == BF16)
             eps = torch.finfo(dtype).eps / 2
             assert ((O[b].cpu().double() - o).abs() <= eps * o.abs() + (1 + eps) * rel * pv + 1e-37).all()
