@@ -91,7 +91,11 @@ int validate(const attn_cache *c, const attn_cache_seqs *s, const attn_cache_fwd
   if (!a->q || !aligned16(a->q)) return ATTN_ERR_INVALID;
   if (!strides_ok(a->dtype, {a->q_stride_b, a->q_stride_s, a->q_stride_h})) return ATTN_ERR_INVALID;
   const long long R = (long long)(a->Hq / c->Hkv) * a->Sq;
-  if (R > INT_MAX / 2 || (R + 7) / 8 * s->B * c->Hkv > INT_MAX) return ATTN_ERR_UNSUPPORTED;  // join grid
+  // Positions of queries stay clear of 32 bits, the join's grid and the count of units
+  // (128 keys of a row tile of 8) within 31.
+  if (a->Sq > (1 << 24) || R > INT_MAX / 2) return ATTN_ERR_UNSUPPORTED;
+  const double units = (double)((R + 7) / 8) * s->B * c->Hkv * ((long long)s->max_pages * c->page_size / kUnit + 1);
+  if (units > INT_MAX) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
 
@@ -117,7 +121,7 @@ FwdParams fwd_params(const attn_cache *c, const attn_cache_seqs *s, const attn_c
   const long long most = std::max(1LL, (long long)p.NG * c->Hkv * ((cap + 31) / 32 * 32 + kUnit - 1) / kUnit);
   p.max_ctas = (int)std::min(most, (mma ? mma_ctas_per_sm(c->D, p.row_tile) : 4LL) * device_sm_count());
   p.causal = a->causal ? 1 : 0;
-  p.window = a->window > 0 ? a->window : 0;
+  p.window = a->window > 0 ? std::min(a->window, 1 << 30) : 0;  // (no sequence is longer)
   p.cap = a->softcap;
   p.inv_cap = a->softcap > 0.f ? 1.f / a->softcap : 0.f;
   p.scale = a->scale;
@@ -133,7 +137,7 @@ FwdParams fwd_params(const attn_cache *c, const attn_cache_seqs *s, const attn_c
   p.w_sh = a->weights_stride_h;
   p.Lpad = (cap + 31) / 32 * 32;
   size_t off = 0;
-  L->prefix = off; off += align_up(((size_t)p.NG + 1) * sizeof(long long));
+  L->prefix = off; off += align_up(((size_t)p.NG + 1) * sizeof(int));
   L->o_part = off; off += align_up((size_t)2 * p.max_ctas * p.row_tile * c->D * sizeof(float));
   L->ml_part = off; off += align_up((size_t)2 * p.max_ctas * p.row_tile * sizeof(float2));
   L->scores = off;
@@ -208,7 +212,7 @@ int attn_cache_fwd(const attn_cache *c, const attn_cache_seqs *s, const attn_cac
   FwdParams p = fwd_params(c, s, a, &L);
   if (!ws || ws_bytes < L.total || ((uintptr_t)ws % kAlign) != 0) return ATTN_ERR_WORKSPACE;
   char *w = static_cast<char *>(ws);
-  p.prefix = reinterpret_cast<long long *>(w + L.prefix);
+  p.prefix = reinterpret_cast<int *>(w + L.prefix);
   p.o_part = reinterpret_cast<float *>(w + L.o_part);
   p.ml_part = reinterpret_cast<float2 *>(w + L.ml_part);
   p.scores = a->weights ? reinterpret_cast<float *>(w + L.scores) : nullptr;

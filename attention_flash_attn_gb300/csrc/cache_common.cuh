@@ -145,7 +145,7 @@ struct FwdParams {
   float *w_out;
   long long w_sb, w_sh;
   // workspace
-  long long *prefix;     // [NG + 1]: units of the groups before each; prefix[NG]: units of one kv head
+  int *prefix;           // [NG + 1]: units of the groups before each; prefix[NG]: units of one kv head
   float *o_part;         // [2 * max_ctas, row_tile, D]: unnormalised partial outputs
   float2 *ml_part;       // [2 * max_ctas, row_tile]: exponent reference (base 2) and sum
   float *scores;         // [B * Hkv, R, Lpad]: logits times log2(e), -inf where unseen
@@ -162,21 +162,31 @@ struct Range {
 __device__ __forceinline__ Range group_range(const FwdParams &p, int b, int rt) {
   Range g;
   g.len = seq_len(p.c, b);
-  const int r0 = rt * p.row_tile, r1 = min(p.R, r0 + p.row_tile) - 1;
-  const long long first = (long long)g.len - p.Sq;  // position of query 0
-  const long long top = first + r1 / p.G, bottom = first + r0 / p.G;
-  g.hi = p.causal && top + 1 < g.len ? (int)(top + 1 < 0 ? 0 : top + 1) : g.len;
+  g.hi = g.len;
   g.lo = 0;
-  if (p.window > 0 && bottom - p.window + 1 > 0) g.lo = (int)(bottom - p.window + 1) & ~31;
-  if (g.lo > g.hi) g.lo = g.hi;  // nothing to see
+  if (p.causal | (p.window > 0)) {
+    const int r0 = rt * p.row_tile, r1 = min(p.R, r0 + p.row_tile) - 1, q0 = g.len - p.Sq;  // position of query 0
+    if (p.causal) g.hi = max(0, min(g.len, q0 + r1 / p.G + 1));
+    if (p.window > 0) g.lo = min(g.hi, max(0, q0 + r0 / p.G - p.window + 1) & ~31);
+  }
   return g;
 }
 __device__ __forceinline__ int range_units(const Range &g) { return (g.hi - g.lo + kUnit - 1) / kUnit; }
 
-// First unit of CTA c's share of U units over C CTAs, and the CTA whose share holds unit u.
-__device__ __forceinline__ long long share_begin(long long c, long long U, long long C) { return c * U / C; }
-__device__ __forceinline__ long long share_owner(long long u, long long U, long long C) { return ((u + 1) * C - 1) / U; }
-__device__ __forceinline__ long long used_ctas(long long U, int max_ctas) { return U < max_ctas ? U : max_ctas; }
+// U units over at most max_ctas CTAs, as evenly as they go: the first `extra` CTAs have one more.
+struct Shares {
+  int C, each, extra;
+  __device__ __forceinline__ Shares(int U, int max_ctas) {
+    C = min(U, max_ctas);
+    each = C ? U / C : 0;
+    extra = U - each * C;
+  }
+  __device__ __forceinline__ int begin(int c) const { return c * each + min(c, extra); }
+  __device__ __forceinline__ int owner(int u) const {  // the CTA whose share holds unit u
+    const int big = extra * (each + 1);
+    return u < big ? u / (each + 1) : extra + (u - big) / each;
+  }
+};
 
 // log2 of the exponentials' unit: logits are kept in base 2.
 constexpr float kLog2e = 1.4426950408889634f;

@@ -73,12 +73,12 @@ __global__ void __launch_bounds__(kThreads) cache_fwd_simt_kernel(const __grid_c
     __syncthreads();
 
     float m[kRows], l[kRows], acc[kRows][NC][4];
-    long long pos_q[kRows];
+    int2 see[kRows];
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       m[r] = -CUDART_INF_F;
       l[r] = 0.f;
-      pos_q[r] = (long long)run.range.len - p.Sq + (r0 + r) / p.G;
+      see[r] = row_sees(p, run.range.len, (r0 + r) / p.G);
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThreads) cache_fwd_simt_kernel(const __grid_c
       bool all = true;
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
-        const bool vis = page >= 0 && r < rows && sees(p, pos_q[r], pos);
+        const bool vis = page >= 0 && r < rows && within(see[r], pos);
         all = all && (vis || r >= rows);
         float u = s[r] * ks;
         if (p.cap > 0.f) u = p.cap * tanhf(u * p.inv_cap);
@@ -245,20 +245,20 @@ __global__ void __launch_bounds__(kThreads) cache_join_kernel(const __grid_const
   const int r = rt * p.row_tile + blockIdx.y;
   if (r >= p.R) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = p.c.D;
-  const long long first = p.prefix[g], n = p.prefix[g + 1] - first, Uh = p.prefix[p.NG];
-  const long long U = Uh * p.c.Hkv, C = used_ctas(U, p.max_ctas), s = hk * Uh + first;
-  long long c0 = 0, c1 = -1;
+  const int first = p.prefix[g], n = p.prefix[g + 1] - first, Uh = p.prefix[p.NG], s = hk * Uh + first;
+  const Shares sh(Uh * p.c.Hkv, p.max_ctas);
+  int c0 = 0, c1 = -1;
   if (n > 0) {
-    c0 = share_owner(s, U, C);
-    c1 = share_owner(s + n - 1, U, C);
+    c0 = sh.owner(s);
+    c1 = sh.owner(s + n - 1);
     if (c0 == c1) return;  // one CTA had the whole item
   }
   // The row's partial of CTA c: the item is the second of the first CTA's two if it begins behind
   // that CTA's first unit, and the first of every later one's.
-  const int second = n > 0 && s > share_begin(c0, U, C) ? 1 : 0;
-  auto part = [&](long long c) { return (size_t)(2 * c + (c == c0 ? second : 0)) * p.row_tile + blockIdx.y; };
+  const int second = n > 0 && s > sh.begin(c0) ? 1 : 0;
+  auto part = [&](int c) { return (size_t)(2 * c + (c == c0 ? second : 0)) * p.row_tile + blockIdx.y; };
   float M = -CUDART_INF_F;
-  for (long long c = c0 + threadIdx.x; c <= c1; c += kThreads) M = max_nan(M, p.ml_part[part(c)].x);
+  for (int c = c0 + threadIdx.x; c <= c1; c += kThreads) M = max_nan(M, p.ml_part[part(c)].x);
   M = warp_max(M);
   if (lane == 0) s_ml[warp].x = M;
   __syncthreads();
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kThreads) cache_join_kernel(const __grid_const
 #pragma unroll
   for (int x = 0; x < 4; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (long long c = c0 + warp; c <= c1; c += kWarps) {
+  for (int c = c0 + warp; c <= c1; c += kWarps) {
     const size_t at = part(c);
     const float2 ml = p.ml_part[at];
     if (ml.x == -CUDART_INF_F) continue;
@@ -315,16 +315,15 @@ __global__ void __launch_bounds__(kThreads) cache_weights_kernel(const __grid_co
   float w[4] = {0.f, 0.f, 0.f, 0.f};
   const float *row = scores_row(p, b, hk, 0) + j0;
   for (int r = 0; r < p.R; ++r, row += p.Lpad) {
-    const long long pos = (long long)len - p.Sq + r / p.G;
     // Scores are stored for the keys that some row of the tile sees (a superset of these).
-    const bool some = (!p.causal || j0 <= pos) && (p.window <= 0 || pos - (j0 + 3) < p.window);
-    if (!some) continue;
+    const int2 see = row_sees(p, len, r / p.G);
+    if (j0 >= see.y || j0 + 3 < see.x) continue;
     const float lse2 = p.LSE[lse_at(p, b, hk, r)] * kLog2e;
     const float4 s = *reinterpret_cast<const float4 *>(row);
     const float t[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
     for (int x = 0; x < 4; ++x)
-      if (j0 + x < len && sees(p, pos, j0 + x)) w[x] += t[x] == -CUDART_INF_F ? 0.f : exp2f(t[x] - lse2);
+      if (within(see, j0 + x)) w[x] += t[x] == -CUDART_INF_F ? 0.f : exp2f(t[x] - lse2);
   }
   const size_t at = (size_t)b * p.w_sb + (size_t)hk * p.w_sh + j0;
 #pragma unroll

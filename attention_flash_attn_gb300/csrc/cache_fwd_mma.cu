@@ -42,11 +42,12 @@ struct Cfg {
   static constexpr int CTAS = MT == 1 ? (D == 64 ? 4 : D == 128 ? 3 : 2) : 2;
   static constexpr bool QREG = D * MT <= 128;          // Q fragments in registers, else in shared memory
   static constexpr int ROWS = 16 * MT;
-  static constexpr int OPITCH = D + 4;
   static constexpr size_t RING = (size_t)kWarps * DEPTH * STAGE;
-  static constexpr size_t O_BYTES = (size_t)ROWS * OPITCH * 4;
+  static_assert(DEPTH * STAGE >= ROWS * D * 4, "a warp's output fits its ring at the end of a run");
   static constexpr size_t Q_BYTES = QREG ? 0 : (size_t)MT * KS * 32 * 16;
-  static constexpr size_t SMEM = 1024 + RING + O_BYTES + Q_BYTES + kWarps * ROWS * 8 + kWarps * DEPTH * 8;
+  static constexpr size_t ML_BYTES = (size_t)kWarps * ROWS * 8;
+  static constexpr size_t NAN_BYTES = (size_t)ROWS * D / 8;  // one bit per output of the run
+  static constexpr size_t SMEM = 1024 + RING + Q_BYTES + ML_BYTES + NAN_BYTES + kWarps * DEPTH * 8;
 };
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int c0, int c1, int c2) {
@@ -101,13 +102,6 @@ template <int KIND> __device__ __forceinline__ void widen4(uint32_t w, uint32_t 
   }
 }
 
-// NaNs of an fp16 pair: *bad has 1.0 in their places, the result 0.
-__device__ __forceinline__ uint32_t split_nan(uint32_t h, uint32_t *bad) {
-  const uint32_t lo = (h & 0x7fffu) > 0x7c00u, hi = (h & 0x7fff0000u) > 0x7c000000u;
-  *bad = (lo ? 0x3c00u : 0u) | (hi ? 0x3c000000u : 0u);
-  return (lo ? 0u : h & 0xffffu) | (hi ? 0u : h & 0xffff0000u);
-}
-
 // cap * tanh(u / cap) * log2(e) with y = 2 log2(e) u / cap: 1 - 2 / (1 + 2^y).  Absolute error some
 // steps of the cap; saturates cleanly (2^y = inf gives 1, 0 gives -1).
 __device__ __forceinline__ float softcap_log2(float y, float cap_log2) {
@@ -120,20 +114,67 @@ template <int BLK> __device__ __forceinline__ uint32_t swz(int row, int ch) {
   return row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
 }
 
+// Makes a slice's values fit to be multiplied by P where some row does not see every key: rows of
+// keys that no row sees (slots behind the last token may hold anything) become 0, and e4m3 NaNs too,
+// after the outputs that they belong to -- of the rows that see their key -- are marked in s_nan.  Only a
+// run's first and last slices come here, so it is kept small rather than fast: one key per lane.
+template <int KIND, int D, int MT>
+__device__ __noinline__ void scrub_values(const FwdParams &p, uint32_t sv, int pos, int key1, unsigned gone, int len, int r0, int rows,
+                                          uint32_t *s_nan, int *s_any) {
+  using C = Cfg<D, MT>;
+  const int lane = threadIdx.x & 31;
+  if (lane < C::SK) {
+    const bool hide = pos + lane >= key1 || ((gone >> (lane >> 4)) & 1u);
+#pragma unroll 1
+    for (int c = 0; c < D / 16; ++c) {
+      const uint32_t at = sv + (c * 16 / C::BLK) * (C::SK * C::BLK) + swz<C::BLK>(lane, c % (C::BLK / 16));
+      uint4 u = lds128(at);
+      uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      bool write = hide;
+      if (hide) {
+        w[0] = w[1] = w[2] = w[3] = 0u;
+      } else if (KIND == ATTN_CACHE_E4M3) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t nan = __vcmpeq4(w[x] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+          if (nan) {
+            write = true;
+#pragma unroll 1
+            for (int r = 0; r < rows; ++r)
+              if (within(row_sees(p, len, (r0 + r) / p.G), pos + lane))
+#pragma unroll 1
+                for (int y = 0; y < 4; ++y)
+                  if ((nan >> (8 * y)) & 1u) {
+                    const int d = c * 16 + x * 4 + y;
+                    atomicOr(s_nan + (r * D + d) / 32, 1u << (d % 32));
+                    *s_any = 1;
+                  }
+            w[x] &= ~nan;
+          }
+        }
+      }
+      if (write) asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+    }
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the stage's next fill comes by TMA
+  __syncwarp();
+}
+
 template <int KIND, int D, int MT>
 __global__ void __launch_bounds__(kThreads, (Cfg<D, MT>::CTAS))
 cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg<D, MT>;
   extern __shared__ uint8_t smem_raw[];
+  __shared__ int s_any;
   const uint32_t raw = smem_u32(smem_raw), ring0 = (raw + 1023u) & ~1023u;
   uint8_t *base = smem_raw + (ring0 - raw);
-  float *s_o = reinterpret_cast<float *>(base + C::RING);                                // [ROWS][OPITCH]
-  uint4 *s_q = reinterpret_cast<uint4 *>(base + C::RING + C::O_BYTES);                   // [MT][KS][32]
-  float2 *s_ml = reinterpret_cast<float2 *>(base + C::RING + C::O_BYTES + C::Q_BYTES);   // [kWarps][ROWS]
+  uint4 *s_q = reinterpret_cast<uint4 *>(base + C::RING);                                      // [MT][KS][32]
+  float2 *s_ml = reinterpret_cast<float2 *>(base + C::RING + C::Q_BYTES);                      // [kWarps][ROWS]
+  uint32_t *s_nan = reinterpret_cast<uint32_t *>(base + C::RING + C::Q_BYTES + C::ML_BYTES);   // [ROWS][D / 32]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t ring = ring0 + warp * (C::DEPTH * C::STAGE);
-  const uint32_t bars = ring0 + C::RING + C::O_BYTES + C::Q_BYTES + kWarps * C::ROWS * 8 + warp * (C::DEPTH * 8);
+  const uint32_t bars = ring0 + C::RING + C::Q_BYTES + C::ML_BYTES + C::NAN_BYTES + warp * (C::DEPTH * 8);
   if (lane == 0) {
 #pragma unroll
     for (int s = 0; s < C::DEPTH; ++s) mbar_init(bars + 8 * s, 1);
@@ -141,6 +182,8 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
   }
+  for (int x = tid; x < C::ROWS * D / 32; x += kThreads) s_nan[x] = 0u;
+  if (tid == 0) s_any = 0;
   __syncwarp();
 
   Cursor cur;
@@ -150,15 +193,15 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
   int stage = 0;
   bool dead = false;    // a wait gave up: recorded; this warp computes no further
   const float cap_log2 = p.cap * kLog2e;
+#pragma unroll 1
   while (cursor_next(p, cur, run)) {
     const int r0 = run.rt * C::ROWS, rows = min(C::ROWS, p.R - r0);
     const int key0 = run.range.lo + run.off * kUnit, key1 = min(run.range.hi, key0 + run.cnt * kUnit);
     // This warp's slices: key0 + (warp + 4 x) SK for x < n_slices.
     const int n_slices = (key1 - key0 - warp * C::SK + kWarps * C::SK - 1) / (kWarps * C::SK);  // <= 0: none
 
-    // Page ids and scales of 32 slices, one per lane: `now` of the batch being consumed, `nxt` of the
-    // following one.
-    int nxt_id[C::NH], id_now[C::NH];
+    // Page ids and scales of 32 slices, one per lane: those of the batch being consumed and of the next.
+    int id_now[C::NH], id_nxt[C::NH];
     float ks_now[C::NH], lv_now[C::NH], inv_now[C::NH], ks_nxt[C::NH], lv_nxt[C::NH], inv_nxt[C::NH];
     auto load_ids = [&](int batch, int *ids) {
       const int x = batch * 32 + lane;
@@ -216,21 +259,17 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
     };
 
     load_ids(0, id_now);
-#pragma unroll
-    for (int s = 0; s < C::DEPTH; ++s)
-      if (s < n_slices) {
-        int st = stage + s;
-        issue(s, st >= C::DEPTH ? st - C::DEPTH : st, id_now);
-      }
+#pragma unroll 1
+    for (int s = 0; s < min(C::DEPTH, n_slices); ++s) issue(s, stage + s >= C::DEPTH ? stage + s - C::DEPTH : stage + s, id_now);
     load_scales(id_now, ks_now, lv_now, inv_now);
 #pragma unroll
-    for (int h = 0; h < C::NH; ++h) nxt_id[h] = -1, ks_nxt[h] = 0.f, lv_nxt[h] = 0.f, inv_nxt[h] = 1.f;
-    if (n_slices > 32) load_ids(1, nxt_id);
+    for (int h = 0; h < C::NH; ++h) id_nxt[h] = -1, ks_nxt[h] = 0.f, lv_nxt[h] = 0.f, inv_nxt[h] = 1.f;
+    if (n_slices > 32) load_ids(1, id_nxt);
 
     // Queries: rows g and g + 8 of each 16, this lane's columns, scaled into fp16.
     uint32_t qf[C::QREG ? MT : 1][C::QREG ? C::KS : 1][4];
     float q_mul[MT][2];  // what undoes the scaling, times the softmax scale (and log2 e without a cap)
-    long long pos_q[MT][2];
+    int see_lo[MT][2], see_n[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       uint4 raw_q[2][D / 32];
@@ -238,22 +277,25 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
       for (int y = 0; y < 2; ++y) {
         const int r = r0 + mt * 16 + 8 * y + g;
         const int i = r / p.G, h = run.hk * p.G + (r - i * p.G);
-        pos_q[mt][y] = (long long)run.range.len - p.Sq + i;
+        const int2 see = row_sees(p, run.range.len, i);
+        see_lo[mt][y] = see.x;
+        see_n[mt][y] = max(0, min(see.y, key1) - see.x);
         float amax = 0.f;
 #pragma unroll
-        for (int j = 0; j < C::NB; ++j)
+        for (int z = 0; z < D / 32; ++z) {
+          raw_q[y][z] = make_uint4(0, 0, 0, 0);
+          if (r < p.R)
+            raw_q[y][z] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + run.b * p.q_sb + i * p.q_ss +
+                                                           h * p.q_sh + (z / (C::BLK / 32)) * C::BLK + t * (C::BLK / 4) +
+                                                           (z % (C::BLK / 32)) * 8);
+        }
 #pragma unroll
-          for (int x = 0; x < C::BLK / 32; ++x) {
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (r < p.R)
-              u = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + run.b * p.q_sb + i * p.q_ss +
-                                                   h * p.q_sh + j * C::BLK + t * (C::BLK / 4) + x * 8);
-            raw_q[y][j * (C::BLK / 32) + x] = u;
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        for (int z = 0; z < D / 32; ++z) {
+          const uint32_t w[4] = {raw_q[y][z].x, raw_q[y][z].y, raw_q[y][z].z, raw_q[y][z].w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              amax = max_nan(amax, max_nan(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
-          }
+          for (int e = 0; e < 4; ++e)
+            amax = max_nan(amax, max_nan(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+        }
         amax = max_nan(amax, __shfl_xor_sync(~0u, amax, 1));
         amax = max_nan(amax, __shfl_xor_sync(~0u, amax, 2));
         // 2^x that brings the largest element into [2^14, 2^15); 1 for rows that are 0 or not finite.
@@ -302,36 +344,35 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
 #pragma unroll
         for (int x = 0; x < 4; ++x) o[mt][n][x] = 0.f;
     }
-    // Positions between which every row of the tile sees a key (rows' positions ascend).
-    const long long first_q = (long long)run.range.len - p.Sq + r0 / p.G, last_q = (long long)run.range.len - p.Sq + (r0 + rows - 1) / p.G;
-    const long long all_below = p.causal ? min((long long)run.range.hi, first_q + 1) : run.range.hi;
-    const long long all_from = p.window > 0 ? last_q - p.window + 1 : 0;
+    // The keys that every row of the tile sees (rows' positions ascend).
+    const int all_from = row_sees(p, run.range.len, (r0 + rows - 1) / p.G).x;
+    const int all_below = min(key1, row_sees(p, run.range.len, r0 / p.G).y);
 
+#pragma unroll 1
     for (int x = 0; x < n_slices; ++x) {
       const int pos = key0 + (warp + kWarps * x) * C::SK;
       if (x > 0 && (x & 31) == 0) {
 #pragma unroll
         for (int h = 0; h < C::NH; ++h) {
-          id_now[h] = nxt_id[h];
+          id_now[h] = id_nxt[h];
           ks_now[h] = ks_nxt[h];
           lv_now[h] = lv_nxt[h];
           inv_now[h] = inv_nxt[h];
         }
-        if (n_slices > (x | 31) + 1) load_ids((x >> 5) + 1, nxt_id);
+        if (n_slices > (x | 31) + 1) load_ids((x >> 5) + 1, id_nxt);
       }
       // This slice's scales.
       float ks[C::NH], lv[C::NH], inv[C::NH];
-      bool zero[C::NH], bad = false, gone[C::NH];
+      unsigned gone = 0, zero = 0;  // bit h: half h has no page; its values count as 0
 #pragma unroll
       for (int h = 0; h < C::NH; ++h) {
         ks[h] = __shfl_sync(~0u, ks_now[h], x & 31);
         lv[h] = __shfl_sync(~0u, lv_now[h], x & 31);
         inv[h] = __shfl_sync(~0u, inv_now[h], x & 31);
-        zero[h] = lv[h] == kZeroLog;
-        gone[h] = __shfl_sync(~0u, id_now[h], x & 31) < 0;
-        bad |= gone[h] | zero[h];
+        gone |= (__shfl_sync(~0u, id_now[h], x & 31) < 0 ? 1u : 0u) << h;
+        zero |= (lv[h] == kZeroLog ? 1u : 0u) << h;
       }
-      const bool partial = bad || pos + C::SK > all_below || pos < all_from;
+      const bool partial = (gone | zero) || pos + C::SK > all_below || pos < all_from;
       const uint32_t sk = ring + stage * C::STAGE, sv = sk + C::SK * D;
       if (!dead) dead = !__all_sync(~0u, mbar_wait(bars + 8 * stage, (phases >> stage) & 1u, p.c.status));
       phases ^= 1u << stage;
@@ -351,7 +392,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
             uint4 kw[C::SK / 8];
 #pragma unroll
             for (int n = 0; n < C::SK / 8; ++n)
-              kw[n] = lds128(sk + j * (C::SK * C::BLK) + swz<C::BLK>(8 * n + g, t * C::CH + c));
+              kw[n] = lds128(sk + j * (C::SK * C::BLK) + n * (8 * C::BLK) + swz<C::BLK>(g, t * C::CH + c));
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
               const int step = (j * C::CH + c) * 4 + w;
@@ -377,33 +418,55 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
             }
           }
         // Softmax: logits in base 2, masked, with the values' scale in the exponent.
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int n = 0; n < C::SK / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[mt][n][e] *= q_mul[mt][e >> 1] * ks[n / 2];
+        if (p.cap > 0.f) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int n = 0; n < C::SK / 8; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[mt][n][e] = softcap_log2(s[mt][n][e], cap_log2);
+        }
+        if (partial) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int n = 0; n < C::SK / 8; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int key = pos + 8 * n + 2 * t + (e & 1);
+                if ((gone >> (n / 2) & 1u) || (unsigned)(key - see_lo[mt][e >> 1]) >= (unsigned)see_n[mt][e >> 1])
+                  s[mt][n][e] = -CUDART_INF_F;
+              }
+          scrub_values<KIND, D, MT>(p, sv, pos, key1, gone | zero, run.range.len, r0, rows, s_nan, &s_any);
+        }
+        if (p.scores) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              if (mt * 16 + 8 * y + g < rows) {
+                float *row = scores_row(p, run.b, run.hk, r0 + mt * 16 + 8 * y + g) + pos + 2 * t;
+#pragma unroll
+                for (int n = 0; n < C::SK / 8; ++n)
+                  *reinterpret_cast<float2 *>(row + 8 * n) = make_float2(s[mt][n][2 * y], s[mt][n][2 * y + 1]);
+              }
+        }
         uint32_t pf[MT][C::NH][4];
         bool moved = false;
         float mn[MT][2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             float top = m[mt][y];
 #pragma unroll
             for (int n = 0; n < C::SK / 8; ++n) {
-              const float f = q_mul[mt][y] * ks[n / 2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float v = s[mt][n][2 * y + e] * f;
-                if (p.cap > 0.f) v = softcap_log2(v, cap_log2);
-                if (partial) {
-                  const int key = pos + 8 * n + 2 * t + e;
-                  if (gone[n / 2] || key >= key1 || !sees(p, pos_q[mt][y], key)) v = -CUDART_INF_F;
-                }
-                s[mt][n][2 * y + e] = v;
-              }
-              if (p.scores) {
-                const int r = mt * 16 + 8 * y + g;
-                if (r < rows)
-                  *reinterpret_cast<float2 *>(scores_row(p, run.b, run.hk, r0 + r) + pos + 8 * n + 2 * t) =
-                      make_float2(s[mt][n][2 * y], s[mt][n][2 * y + 1]);
-              }
               s[mt][n][2 * y] += lv[n / 2];
               s[mt][n][2 * y + 1] += lv[n / 2];
               top = max_nan(top, max_nan(s[mt][n][2 * y], s[mt][n][2 * y + 1]));
@@ -413,7 +476,6 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
             mn[mt][y] = top;
             moved |= top != m[mt][y];
           }
-        }
         if (__any_sync(~0u, moved)) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
@@ -439,7 +501,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
               const float ref = m[mt][y] == -CUDART_INF_F ? 0.f : m[mt][y];
               const float e0 = ex2(s[mt][n][2 * y] - ref), e1 = ex2(s[mt][n][2 * y + 1] - ref);
               l[mt][y] += (e0 + e1) * inv[h];
-              pf[mt][h][q] = zero[h] ? 0u : pack_h2(e0, e1);
+              pf[mt][h][q] = pack_h2(e0, e1);
             }
         // O += P V: lane t has keys 2t, 2t + 1, 2t + 8, 2t + 9 of each 16 as the B operand's rows, and
         // BLK / 8 neighbouring columns, one for each n-tile.
@@ -450,23 +512,18 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
             uint32_t vw[4][C::BLK / 32];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const int key = 16 * h + 2 * t + (q & 1) + 8 * (q >> 1);
-              const uint32_t at = sv + j * (C::SK * C::BLK);
+              // Key 16 h + 8 (q >> 1) + 2 t + (q & 1): its low three bits, which the swizzle uses, are the last two terms.
+              const uint32_t at = sv + j * (C::SK * C::BLK) + (16 * h + 8 * (q >> 1)) * C::BLK;
               if (C::BLK == 128) {
-                const uint4 u = lds128(at + swz<C::BLK>(key, g));
+                const uint4 u = lds128(at + swz<C::BLK>(2 * t + (q & 1), g));
                 vw[q][0] = u.x;
                 vw[q][1] = u.y;
                 vw[q][C::BLK / 32 - 2] = u.z;
                 vw[q][C::BLK / 32 - 1] = u.w;
               } else {
-                const uint2 u = lds64(at + swz<C::BLK>(key, g >> 1) + (g & 1) * 8);
+                const uint2 u = lds64(at + swz<C::BLK>(2 * t + (q & 1), g >> 1) + (g & 1) * 8);
                 vw[q][0] = u.x;
                 vw[q][1] = u.y;
-              }
-              // Slots that hold no token of the sequence may hold anything.
-              if (partial && (gone[h] || zero[h] || pos + key >= key1)) {
-#pragma unroll
-                for (int w = 0; w < C::BLK / 32; ++w) vw[q][w] = 0u;
               }
             }
 #pragma unroll
@@ -478,126 +535,100 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
                 widen4<KIND>(__byte_perm(vw[0][w], vw[1][w], sel), b0[0], b0[1]);
                 widen4<KIND>(__byte_perm(vw[2][w], vw[3][w], sel), b1[0], b1[1]);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int n = j * (C::BLK / 8) + 4 * w + 2 * z + e;
-                  if (KIND == ATTN_CACHE_E4M3 && partial) {
-                    // A NaN value reaches the rows that see its key, and no other: its place counts as 0
-                    // in the product, and a product of what rows see with where NaNs are tells them.
-                    uint32_t n0, n1;
-                    const uint32_t c0 = split_nan(b0[e], &n0), c1 = split_nan(b1[e], &n1);
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                      uint32_t see[4];
-#pragma unroll
-                      for (int q = 0; q < 4; ++q) {
-                        const int k0 = pos + 16 * h + 2 * t + 8 * (q >> 1);
-                        see[q] = (k0 < key1 && sees(p, pos_q[mt][q & 1], k0) ? 0x3c00u : 0u) |
-                                 (k0 + 1 < key1 && sees(p, pos_q[mt][q & 1], k0 + 1) ? 0x3c000000u : 0u);
-                      }
-                      float hit[4] = {0.f, 0.f, 0.f, 0.f};
-                      mma_f16(hit, see, n0, n1);
-                      mma_f16(o[mt][n], pf[mt][h], c0, c1);
-#pragma unroll
-                      for (int q = 0; q < 4; ++q)
-                        if (hit[q] > 0.f) o[mt][n][q] = CUDART_NAN_F;
-                    }
-                  } else {
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) mma_f16(o[mt][n], pf[mt][h], b0[e], b1[e]);
-                  }
-                }
+                  for (int mt = 0; mt < MT; ++mt) mma_f16(o[mt][j * (C::BLK / 8) + 4 * w + 2 * z + e], pf[mt][h], b0[e], b1[e]);
               }
           }
       }
       __syncwarp();  // every lane has read the stage
       if (x + C::DEPTH < n_slices && !dead) {
         const int y = x + C::DEPTH;
-        if ((y & 31) == 0) load_scales(nxt_id, ks_nxt, lv_nxt, inv_nxt);
-        issue(y, stage, (y >> 5) == (x >> 5) ? id_now : nxt_id);
+        if ((y & 31) == 0) load_scales(id_nxt, ks_nxt, lv_nxt, inv_nxt);
+        issue(y, stage, (y >> 5) == (x >> 5) ? id_now : id_nxt);
       }
       stage = stage + 1 == C::DEPTH ? 0 : stage + 1;
     }
 
-    // The four warps' rows joined in shared memory, and the run's end.
+    // The run's end: each warp leaves its rows in its ring (nothing is in flight), four columns at a time,
+    // the 16-byte groups permuted so that the lanes of a store meet different banks; then all threads add
+    // the four warps' rows up.
+    auto o_at = [](int r, int d) {  // float index of row r, column d (a multiple of 4)
+      return r * D + ((d >> 2) ^ (4 * (r & 1) + ((d / (C::BLK / 4)) & 3))) * 4;
+    };
+    {
+      float *my = reinterpret_cast<float *>(base + warp * (C::DEPTH * C::STAGE));
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        float v = l[mt][y];
-        v += __shfl_xor_sync(~0u, v, 1);
-        v += __shfl_xor_sync(~0u, v, 2);
-        if (dead) v = CUDART_NAN_F;
-        if (t == 0) s_ml[warp * C::ROWS + mt * 16 + 8 * y + g] = make_float2(m[mt][y], v);
-      }
-    __syncthreads();
-    float f[MT][2];
+        for (int y = 0; y < 2; ++y) {
+          const int r = mt * 16 + 8 * y + g;
+          float v = l[mt][y];
+          v += __shfl_xor_sync(~0u, v, 1);
+          v += __shfl_xor_sync(~0u, v, 2);
+          if (t == 0) s_ml[warp * C::ROWS + r] = make_float2(m[mt][y], dead ? CUDART_NAN_F : v);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+          for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        float M = -CUDART_INF_F;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) M = max_nan(M, s_ml[w * C::ROWS + mt * 16 + 8 * y + g].x);
-        f[mt][y] = m[mt][y] == -CUDART_INF_F ? 0.f : ex2(m[mt][y] - M);
-      }
-    for (int w = 0; w < kWarps; ++w) {
-      if (warp == w) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int n = 0; n < C::NT; n += 4) {
-                // n-tile n of a block: column (BLK / 8) (2 t + e) + n.
-                const int j = n / (C::BLK / 8), d = j * C::BLK + (C::BLK / 8) * (2 * t + e) + n % (C::BLK / 8);
-                float4 *at = reinterpret_cast<float4 *>(s_o + (mt * 16 + 8 * y + g) * C::OPITCH + d);
-                float4 v = w ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
-                if (f[mt][y] != 0.f) {
-                  v.x += f[mt][y] * o[mt][n][2 * y + e];
-                  v.y += f[mt][y] * o[mt][n + 1][2 * y + e];
-                  v.z += f[mt][y] * o[mt][n + 2][2 * y + e];
-                  v.w += f[mt][y] * o[mt][n + 3][2 * y + e];
-                }
-                *at = v;
-              }
-      }
-      __syncthreads();
+            for (int n = 0; n < C::NT; n += 4) {
+              // n-tile n of a block: column (BLK / 8) (2 t + e) + n.
+              const int j = n / (C::BLK / 8), d = j * C::BLK + (C::BLK / 8) * (2 * t + e) + n % (C::BLK / 8);
+              *reinterpret_cast<float4 *>(my + o_at(r, d)) =
+                  make_float4(o[mt][n][2 * y + e], o[mt][n + 1][2 * y + e], o[mt][n + 2][2 * y + e], o[mt][n + 3][2 * y + e]);
+            }
+        }
     }
-    const bool whole = run.cnt == run.n;
-    for (int r = warp; r < rows; r += kWarps) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring's next fill comes by TMA
+    __syncthreads();
+    const bool whole = run.cnt == run.n, nans = s_any != 0;
+#pragma unroll 1
+    for (int x = tid; x < rows * (D / 4); x += kThreads) {
+      const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+      float2 ml[kWarps];
       float M = -CUDART_INF_F, L = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = max_nan(M, s_ml[w * C::ROWS + r].x);
+      for (int w = 0; w < kWarps; ++w) {
+        ml[w] = s_ml[w * C::ROWS + r];
+        M = max_nan(M, ml[w].x);
+      }
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float2 ml = s_ml[w * C::ROWS + r];
-        if (ml.x != -CUDART_INF_F) L += ml.y * ex2(ml.x - M);
+        if (ml[w].x == -CUDART_INF_F) continue;
+        const float f = ex2(ml[w].x - M);
+        const float4 u = *reinterpret_cast<const float4 *>(base + w * (C::DEPTH * C::STAGE) + o_at(r, d) * 4);
+        L += f * ml[w].y;
+        v.x += f * u.x;
+        v.y += f * u.y;
+        v.z += f * u.z;
+        v.w += f * u.w;
       }
-      float scale = 1.f;
+      if (nans) {
+        const uint32_t bits = s_nan[(r * D + d) / 32] >> (d % 32);
+        if (bits & 1u) v.x = CUDART_NAN_F;
+        if (bits & 2u) v.y = CUDART_NAN_F;
+        if (bits & 4u) v.z = CUDART_NAN_F;
+        if (bits & 8u) v.w = CUDART_NAN_F;
+      }
       if (whole) {
         const RowEnd e = row_end(p, run.hk * p.G + (r0 + r) % p.G, M, L);
-        scale = e.scale;
-        if (lane == 0) p.LSE[lse_at(p, run.b, run.hk, r0 + r)] = e.lse;
-      } else if (lane == 0) {
-        p.ml_part[(size_t)run.slot * C::ROWS + r] = make_float2(M, L);
-      }
-      for (int d = lane * 4; d < D; d += 128) {
-        float4 v = *reinterpret_cast<const float4 *>(s_o + r * C::OPITCH + d);
-        if (whole) {
-          if (M == -CUDART_INF_F) v = make_float4(0.f, 0.f, 0.f, 0.f);
-          uint2 u;
-          __nv_bfloat162 a = __floats2bfloat162_rn(v.x * scale, v.y * scale), b = __floats2bfloat162_rn(v.z * scale, v.w * scale);
-          u.x = *reinterpret_cast<uint32_t *>(&a);
-          u.y = *reinterpret_cast<uint32_t *>(&b);
-          *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.O) + o_row(p, run.b, run.hk, r0 + r) + d) = u;
-        } else {
-          *reinterpret_cast<float4 *>(p.o_part + ((size_t)run.slot * C::ROWS + r) * D + d) = v;
-        }
+        if (d == 0) p.LSE[lse_at(p, run.b, run.hk, r0 + r)] = e.lse;
+        __nv_bfloat162 a = __floats2bfloat162_rn(v.x * e.scale, v.y * e.scale), b = __floats2bfloat162_rn(v.z * e.scale, v.w * e.scale);
+        uint2 u;
+        u.x = *reinterpret_cast<uint32_t *>(&a);
+        u.y = *reinterpret_cast<uint32_t *>(&b);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.O) + o_row(p, run.b, run.hk, r0 + r) + d) = u;
+      } else {
+        if (d == 0) p.ml_part[(size_t)run.slot * C::ROWS + r] = make_float2(M, L);
+        *reinterpret_cast<float4 *>(p.o_part + ((size_t)run.slot * C::ROWS + r) * D + d) = v;
       }
     }
-    __syncthreads();  // s_o and s_ml are free for the next run
+    __syncthreads();  // the ring, s_ml and s_nan are free for the next run
+    if (nans) {
+      for (int x = tid; x < C::ROWS * D / 32; x += kThreads) s_nan[x] = 0u;
+      if (tid == 0) s_any = 0;
+      __syncthreads();
+    }
   }
 }
 

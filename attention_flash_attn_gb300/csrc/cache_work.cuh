@@ -20,12 +20,12 @@ namespace cache {
 
 constexpr int kThreads = 128;
 
-// The units of a CTA, item by item.
+// The units of a CTA, item by item.  Unit counts fit 31 bits (checked on the host).
 struct Cursor {
-  long long Uh;        // units of one kv head
-  long long u0, u, u1; // this CTA's units; u: the next one
-  int hk, g;           // item of unit u
-  long long g_first;   // first unit of that item
+  int Uh;         // units of one kv head
+  int u0, u, u1;  // this CTA's units; u: the next one
+  int hk, g;      // item of unit u
+  int g_first;    // first unit of that item
 };
 
 // A run of units [off, off + cnt) of item (hk, b, rt), which has n of them.
@@ -34,73 +34,79 @@ struct Run {
   Range range;
 };
 
+__device__ __forceinline__ int group_units(const FwdParams &p, int g) {
+  const int b = p.RT == 1 ? g : g / p.RT;
+  return range_units(group_range(p, b, g - b * p.RT));
+}
+
 // Called by all kThreads threads; false if this CTA has no units.  CTA 0 stores the prefix sums and
-// records lengths outside the table.
+// records lengths outside the table.  Each thread has a contiguous part of the groups.
 __device__ __forceinline__ bool cursor_begin(const FwdParams &p, Cursor &cur) {
-  __shared__ long long s_sum[kThreads / 32];
-  __shared__ long long s_first;
-  __shared__ int s_g;
-  const int t = threadIdx.x;
-  const int g0 = (int)((long long)t * p.NG / kThreads), g1 = (int)((long long)(t + 1) * p.NG / kThreads);
-  long long sum = 0;
-  for (int g = g0; g < g1; ++g) sum += range_units(group_range(p, g / p.RT, g % p.RT));
-  long long incl = sum;
+  __shared__ int s_sum[kThreads / 32], s_at[2];
+  const int t = threadIdx.x, per = (p.NG + kThreads - 1) / kThreads;
+  const int g0 = min(p.NG, t * per), g1 = min(p.NG, g0 + per);
+  int sum = 0;
+#pragma unroll 1
+  for (int g = g0; g < g1; ++g) sum += group_units(p, g);
+  int incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(~0u, incl, o);
+    const int v = __shfl_up_sync(~0u, incl, o);
     if ((t & 31) >= o) incl += v;
   }
   if ((t & 31) == 31) s_sum[t >> 5] = incl;
   __syncthreads();
-  long long before = 0, Uh = 0;
+  int excl = incl - sum, Uh = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < (t >> 5)) before += s_sum[w];
+    if (w < (t >> 5)) excl += s_sum[w];
     Uh += s_sum[w];
   }
-  const long long excl = before + incl - sum;
   if (blockIdx.x == 0) {
-    long long x = excl;
+    int x = excl;
+#pragma unroll 1
     for (int g = g0; g < g1; ++g) {
       p.prefix[g] = x;
-      x += range_units(group_range(p, g / p.RT, g % p.RT));
+      x += group_units(p, g);
     }
     if (t == kThreads - 1) p.prefix[p.NG] = Uh;
+#pragma unroll 1
     for (int b = t; b < p.c.B; b += kThreads) {
       bool bad;
       seq_len(p.c, b, &bad);
       if (bad) set_status(p.c.status, kStatusBadPage);
     }
   }
-  const long long U = Uh * p.c.Hkv, C = used_ctas(U, p.max_ctas);
-  if (blockIdx.x >= C) return false;
+  const Shares sh(Uh * p.c.Hkv, p.max_ctas);
+  if (blockIdx.x >= sh.C) return false;
   cur.Uh = Uh;
-  cur.u0 = cur.u = share_begin(blockIdx.x, U, C);
-  cur.u1 = share_begin(blockIdx.x + 1, U, C);
-  cur.hk = (int)(cur.u / Uh);
-  const long long r = cur.u - cur.hk * Uh;
+  cur.u0 = cur.u = sh.begin(blockIdx.x);
+  cur.u1 = sh.begin(blockIdx.x + 1);
+  cur.hk = cur.u / Uh;
+  const int r = cur.u - cur.hk * Uh;
   if (excl <= r && r < excl + sum) {
-    long long x = excl;
-    int g = g0;
+    int x = excl, g = g0;
+#pragma unroll 1
     for (;; ++g) {
-      const int n = range_units(group_range(p, g / p.RT, g % p.RT));
+      const int n = group_units(p, g);
       if (r < x + n) break;
       x += n;
     }
-    s_g = g;
-    s_first = x;
+    s_at[0] = g;
+    s_at[1] = x;
   }
   __syncthreads();
-  cur.g = s_g;
-  cur.g_first = cur.hk * Uh + s_first;
+  cur.g = s_at[0];
+  cur.g_first = cur.hk * Uh + s_at[1];
   return true;
 }
 
 // The next run of this CTA; false when there is none.  Uniform over the CTA.
 __device__ __forceinline__ bool cursor_next(const FwdParams &p, Cursor &cur, Run &run) {
   if (cur.u >= cur.u1) return false;
+#pragma unroll 1
   for (;;) {
-    run.b = cur.g / p.RT;
+    run.b = p.RT == 1 ? cur.g : cur.g / p.RT;
     run.rt = cur.g - run.b * p.RT;
     run.range = group_range(p, run.b, run.rt);
     run.n = range_units(run.range);
@@ -112,19 +118,19 @@ __device__ __forceinline__ bool cursor_next(const FwdParams &p, Cursor &cur, Run
     }
   }
   run.hk = cur.hk;
-  run.off = (int)(cur.u - cur.g_first);
-  const long long left = cur.u1 - cur.u;
-  run.cnt = (int)(run.n - run.off < left ? run.n - run.off : left);
+  run.off = cur.u - cur.g_first;
+  run.cnt = min(run.n - run.off, cur.u1 - cur.u);
   run.slot = 2 * blockIdx.x + (cur.g_first > cur.u0 ? 1 : 0);
   cur.u += run.cnt;
   return true;
 }
 
-// Whether a row at position pos_q sees key pos (below the row tile's hi).
-__device__ __forceinline__ bool sees(const FwdParams &p, long long pos_q, int pos) {
-  if (p.causal && pos > pos_q) return false;
-  return p.window <= 0 || pos_q - pos < p.window;
+// The keys [lo, hi) that query i of a sequence of `len` tokens sees.
+__device__ __forceinline__ int2 row_sees(const FwdParams &p, int len, int i) {
+  const int pos = len - p.Sq + i;
+  return make_int2(p.window > 0 ? max(0, pos - p.window + 1) : 0, p.causal ? max(0, min(len, pos + 1)) : len);
 }
+__device__ __forceinline__ bool within(int2 see, int key) { return key >= see.x && key < see.y; }
 
 // The logarithm (base 2) of a page's value scale, and its inverse; scales below 2^-60 count as 0.
 __device__ __forceinline__ float scale_log2(float vs, float *inv, bool *zero) {

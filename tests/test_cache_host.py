@@ -288,7 +288,7 @@ def test_eviction_arguments_of_the_binding():
 # ---------------------------------------------------------------- shares of work
 
 def test_every_unit_has_one_owner_and_every_split_item_its_parts():
-    """The units of all items are shared out by c * U // C; the join finds an item's CTAs by ((u + 1) * C - 1) // U and a
+    """U units over C CTAs: U // C each and one more for the first U % C.  The join finds an item's CTAs by the inverse, and a
     CTA's second partial by where the item begins.  Here the same arithmetic, against a walk over the shares."""
     rng = random.Random(3)
     for _ in range(400):
@@ -297,7 +297,11 @@ def test_every_unit_has_one_owner_and_every_split_item_its_parts():
         C = min(U, most)
         if U == 0:
             continue
-        begin = [c * U // C for c in range(C + 1)]
+        each, extra = divmod(U, C)
+        begin = [c * each + min(c, extra) for c in range(C + 1)]
+        big = extra * (each + 1)
+        owner = lambda u: u // (each + 1) if u < big else extra + (u - big) // each  # noqa: E731
+        assert begin[C] == U and all(begin[owner(u)] <= u < begin[owner(u) + 1] for u in range(U))
         parts, slots = {}, set()
         for c in range(C):
             assert begin[c] < begin[c + 1]
@@ -316,7 +320,7 @@ def test_every_unit_has_one_owner_and_every_split_item_its_parts():
         first = 0
         for it, n in enumerate(items):
             if n:
-                c0, c1 = ((first + 1) * C - 1) // U, ((first + n) * C - 1) // U
+                c0, c1 = owner(first), owner(first + n - 1)
                 want = [] if c0 == c1 else [2 * c + (1 if c == c0 and first > begin[c0] else 0) for c in range(c0, c1 + 1)]
                 assert parts.get(it, []) == want
             first += n
