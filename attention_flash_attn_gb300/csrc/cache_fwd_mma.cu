@@ -25,7 +25,7 @@ namespace {
 using namespace attn::tc;
 
 constexpr int kWarps = kThreads / 32;
-constexpr float kZeroLog = kMinScaleExp - 1, kZeroInv = 2.f / kMinScale;
+constexpr float kZeroLog = kMinScaleExp - 1;
 
 template <int D_, int MT_>
 struct Cfg {
@@ -40,7 +40,7 @@ struct Cfg {
   static constexpr int STAGE = 2 * SK * D;             // bytes of a slice, K then V
   static constexpr int DEPTH = D == 64 ? (MT == 1 ? 3 : 4) : 2;
   static constexpr int CTAS = MT == 1 ? (D == 64 ? 4 : D == 128 ? 3 : 2) : 2;
-  static constexpr bool QREG = D * MT <= 128;          // Q fragments in registers, else in shared memory
+  static constexpr bool QREG = D * MT <= 64;           // Q fragments in registers, else in shared memory
   static constexpr int ROWS = 16 * MT;
   static constexpr size_t RING = (size_t)kWarps * DEPTH * STAGE;
   static_assert(DEPTH * STAGE >= ROWS * D * 4, "a warp's output fits its ring at the end of a run");
@@ -200,9 +200,10 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
     // This warp's slices: key0 + (warp + 4 x) SK for x < n_slices.
     const int n_slices = (key1 - key0 - warp * C::SK + kWarps * C::SK - 1) / (kWarps * C::SK);  // <= 0: none
 
-    // Page ids and scales of 32 slices, one per lane: those of the batch being consumed and of the next.
+    // Page ids and scales of 32 slices, one per lane, and the following batch's page ids.
     int id_now[C::NH], id_nxt[C::NH];
-    float ks_now[C::NH], lv_now[C::NH], inv_now[C::NH], ks_nxt[C::NH], lv_nxt[C::NH], inv_nxt[C::NH];
+    float ks_now[C::NH], lv_now[C::NH];
+    unsigned odd_now = 0;  // bit x: slice x of the batch has a half without a page, or whose values count as 0
     auto load_ids = [&](int batch, int *ids) {
       const int x = batch * 32 + lane;
 #pragma unroll
@@ -211,24 +212,23 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
         ids[h] = x < n_slices && pos < key1 ? page_of(p.c, run.b, pos) : -1;
       }
     };
-    // (A value scale that counts as 0 has kZeroLog for its logarithm.)
-    auto load_scales = [&](const int *ids, float *ks, float *lv, float *inv) {
+    // A value scale that counts as 0 has kZeroLog for its logarithm: any reference does for values of 0, as
+    // long as the sum undoes it.
+    auto load_scales = [&]() {
+      bool odd = false;
 #pragma unroll
       for (int h = 0; h < C::NH; ++h) {
-        ks[h] = 0.f;
-        float vs = 1.f;
-        if (ids[h] >= 0) {
-          const size_t at = (size_t)ids[h] * p.c.Hkv + run.hk;
-          ks[h] = p.c.k_scale[at];
+        ks_now[h] = 0.f;
+        float vs = 0.f;
+        if (id_now[h] >= 0) {
+          const size_t at = (size_t)id_now[h] * p.c.Hkv + run.hk;
+          ks_now[h] = p.c.k_scale[at];
           vs = p.c.v_scale[at];
         }
-        bool zero;
-        lv[h] = scale_log2(vs, &inv[h], &zero);
-        if (zero) {  // any reference does for values of 0, if the sum undoes it
-          lv[h] = kZeroLog;
-          inv[h] = kZeroInv;
-        }
+        lv_now[h] = vs >= kMinScale ? log2f(vs) : kZeroLog;
+        odd |= !(vs >= kMinScale);
       }
+      odd_now = __ballot_sync(~0u, odd);
     };
     // Fills ring stage `st` with slice x (ids: its batch).  All lanes call it; lane 0 issues.
     auto issue = [&](int x, int st, const int *ids) {
@@ -261,9 +261,9 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
     load_ids(0, id_now);
 #pragma unroll 1
     for (int s = 0; s < min(C::DEPTH, n_slices); ++s) issue(s, stage + s >= C::DEPTH ? stage + s - C::DEPTH : stage + s, id_now);
-    load_scales(id_now, ks_now, lv_now, inv_now);
+    load_scales();
 #pragma unroll
-    for (int h = 0; h < C::NH; ++h) id_nxt[h] = -1, ks_nxt[h] = 0.f, lv_nxt[h] = 0.f, inv_nxt[h] = 1.f;
+    for (int h = 0; h < C::NH; ++h) id_nxt[h] = -1;
     if (n_slices > 32) load_ids(1, id_nxt);
 
     // Queries: rows g and g + 8 of each 16, this lane's columns, scaled into fp16.
@@ -302,8 +302,8 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
         int x = 14 - ((int)(__float_as_uint(amax) >> 23) - 127);
         if (!(amax > 0.f) || !(amax <= 3.402823466e38f)) x = 0;
         x = x > 126 ? 126 : x;
-        const float up = __uint_as_float((unsigned)(x + 127) << 23);
-        q_mul[mt][y] = __uint_as_float((unsigned)(127 - x) << 23) * p.scale * (p.cap > 0.f ? 2.f * kLog2e * p.inv_cap : kLog2e);
+        const float up = copysignf(__uint_as_float((unsigned)(x + 127) << 23), p.scale);
+        q_mul[mt][y] = __uint_as_float((unsigned)(127 - x) << 23) * fabsf(p.scale) * (p.cap > 0.f ? 2.f * kLog2e * p.inv_cap : kLog2e);
 #pragma unroll
         for (int z = 0; z < D / 32; ++z) {
           uint4 &u = raw_q[y][z];
@@ -353,26 +353,18 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
       const int pos = key0 + (warp + kWarps * x) * C::SK;
       if (x > 0 && (x & 31) == 0) {
 #pragma unroll
-        for (int h = 0; h < C::NH; ++h) {
-          id_now[h] = id_nxt[h];
-          ks_now[h] = ks_nxt[h];
-          lv_now[h] = lv_nxt[h];
-          inv_now[h] = inv_nxt[h];
-        }
+        for (int h = 0; h < C::NH; ++h) id_now[h] = id_nxt[h];
+        load_scales();
         if (n_slices > (x | 31) + 1) load_ids((x >> 5) + 1, id_nxt);
       }
       // This slice's scales.
-      float ks[C::NH], lv[C::NH], inv[C::NH];
-      unsigned gone = 0, zero = 0;  // bit h: half h has no page; its values count as 0
+      float ks[C::NH], lv[C::NH];
 #pragma unroll
       for (int h = 0; h < C::NH; ++h) {
         ks[h] = __shfl_sync(~0u, ks_now[h], x & 31);
         lv[h] = __shfl_sync(~0u, lv_now[h], x & 31);
-        inv[h] = __shfl_sync(~0u, inv_now[h], x & 31);
-        gone |= (__shfl_sync(~0u, id_now[h], x & 31) < 0 ? 1u : 0u) << h;
-        zero |= (lv[h] == kZeroLog ? 1u : 0u) << h;
       }
-      const bool partial = (gone | zero) || pos + C::SK > all_below || pos < all_from;
+      const bool partial = ((odd_now >> (x & 31)) & 1u) || pos + C::SK > all_below || pos < all_from;
       const uint32_t sk = ring + stage * C::STAGE, sv = sk + C::SK * D;
       if (!dead) dead = !__all_sync(~0u, mbar_wait(bars + 8 * stage, (phases >> stage) & 1u, p.c.status));
       phases ^= 1u << stage;
@@ -417,33 +409,56 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
               }
             }
           }
-        // Softmax: logits in base 2, masked, with the values' scale in the exponent.
+        // Softmax.  A probability is 2^(f s + lv - m): f takes a raw score to a logit in base 2 (it is not
+        // negative, so that the largest raw score gives the largest logit), lv is the values' scale.  With a cap
+        // or a mask the logits are formed first, and f is 1.
+        float f[MT][2][C::NH];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int n = 0; n < C::SK / 8; ++n)
+          for (int y = 0; y < 2; ++y)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[mt][n][e] *= q_mul[mt][e >> 1] * ks[n / 2];
-        if (p.cap > 0.f) {
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int n = 0; n < C::SK / 8; ++n)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) s[mt][n][e] = softcap_log2(s[mt][n][e], cap_log2);
-        }
-        if (partial) {
+            for (int h = 0; h < C::NH; ++h) f[mt][y][h] = q_mul[mt][y] * ks[h];
+        if (partial || p.cap > 0.f) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int n = 0; n < C::SK / 8; ++n)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int key = pos + 8 * n + 2 * t + (e & 1);
-                if ((gone >> (n / 2) & 1u) || (unsigned)(key - see_lo[mt][e >> 1]) >= (unsigned)see_n[mt][e >> 1])
-                  s[mt][n][e] = -CUDART_INF_F;
-              }
-          scrub_values<KIND, D, MT>(p, sv, pos, key1, gone | zero, run.range.len, r0, rows, s_nan, &s_any);
+              for (int e = 0; e < 4; ++e) s[mt][n][e] *= f[mt][e >> 1][n / 2];
+          if (p.cap > 0.f) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int n = 0; n < C::SK / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[mt][n][e] = softcap_log2(s[mt][n][e], cap_log2);
+          }
+          if (partial) {
+            unsigned gone = 0, zero = 0;  // bit h: half h has no page; its values count as 0
+#pragma unroll
+            for (int h = 0; h < C::NH; ++h) {
+              gone |= (__shfl_sync(~0u, id_now[h], x & 31) < 0 ? 1u : 0u) << h;
+              zero |= (lv[h] == kZeroLog ? 1u : 0u) << h;
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int n = 0; n < C::SK / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int key = pos + 8 * n + 2 * t + (e & 1);
+                  if ((gone >> (n / 2) & 1u) || (unsigned)(key - see_lo[mt][e >> 1]) >= (unsigned)see_n[mt][e >> 1])
+                    s[mt][n][e] = -CUDART_INF_F;
+                }
+            scrub_values<KIND, D, MT>(p, sv, pos, key1, gone | zero, run.range.len, r0, rows, s_nan, &s_any);
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+              for (int h = 0; h < C::NH; ++h) f[mt][y][h] = 1.f;
         }
         if (p.scores) {
 #pragma unroll
@@ -454,7 +469,8 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
                 float *row = scores_row(p, run.b, run.hk, r0 + mt * 16 + 8 * y + g) + pos + 2 * t;
 #pragma unroll
                 for (int n = 0; n < C::SK / 8; ++n)
-                  *reinterpret_cast<float2 *>(row + 8 * n) = make_float2(s[mt][n][2 * y], s[mt][n][2 * y + 1]);
+                  *reinterpret_cast<float2 *>(row + 8 * n) =
+                      make_float2(f[mt][y][n / 2] * s[mt][n][2 * y], f[mt][y][n / 2] * s[mt][n][2 * y + 1]);
               }
         }
         uint32_t pf[MT][C::NH][4];
@@ -466,10 +482,9 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
           for (int y = 0; y < 2; ++y) {
             float top = m[mt][y];
 #pragma unroll
-            for (int n = 0; n < C::SK / 8; ++n) {
-              s[mt][n][2 * y] += lv[n / 2];
-              s[mt][n][2 * y + 1] += lv[n / 2];
-              top = max_nan(top, max_nan(s[mt][n][2 * y], s[mt][n][2 * y + 1]));
+            for (int h = 0; h < C::NH; ++h) {
+              const float a = max_nan(s[mt][2 * h][2 * y], s[mt][2 * h][2 * y + 1], s[mt][2 * h + 1][2 * y]);
+              top = max_nan(top, fmaf(f[mt][y][h], max_nan(a, s[mt][2 * h + 1][2 * y + 1]), lv[h]));
             }
             top = max_nan(top, __shfl_xor_sync(~0u, top, 1));
             top = max_nan(top, __shfl_xor_sync(~0u, top, 2));
@@ -492,17 +507,21 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
             }
         }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int h = 0; h < C::NH; ++h) {
+          const float inv = ex2(-lv[h]);
 #pragma unroll
-          for (int h = 0; h < C::NH; ++h)
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int y = q & 1, n = 2 * h + (q >> 1);
-              const float ref = m[mt][y] == -CUDART_INF_F ? 0.f : m[mt][y];
-              const float e0 = ex2(s[mt][n][2 * y] - ref), e1 = ex2(s[mt][n][2 * y + 1] - ref);
-              l[mt][y] += (e0 + e1) * inv[h];
-              pf[mt][h][q] = pack_h2(e0, e1);
+            for (int y = 0; y < 2; ++y) {
+              const float ref = lv[h] - (m[mt][y] == -CUDART_INF_F ? 0.f : m[mt][y]);
+              float e[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) e[q] = ex2(fmaf(f[mt][y][h], s[mt][2 * h + (q >> 1)][2 * y + (q & 1)], ref));
+              l[mt][y] = fmaf((e[0] + e[1]) + (e[2] + e[3]), inv, l[mt][y]);
+              pf[mt][h][y] = pack_h2(e[0], e[1]);
+              pf[mt][h][2 + y] = pack_h2(e[2], e[3]);
             }
+        }
         // O += P V: lane t has keys 2t, 2t + 1, 2t + 8, 2t + 9 of each 16 as the B operand's rows, and
         // BLK / 8 neighbouring columns, one for each n-tile.
 #pragma unroll
@@ -544,7 +563,6 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
       __syncwarp();  // every lane has read the stage
       if (x + C::DEPTH < n_slices && !dead) {
         const int y = x + C::DEPTH;
-        if ((y & 31) == 0) load_scales(id_nxt, ks_nxt, lv_nxt, inv_nxt);
         issue(y, stage, (y >> 5) == (x >> 5) ? id_now : id_nxt);
       }
       stage = stage + 1 == C::DEPTH ? 0 : stage + 1;
