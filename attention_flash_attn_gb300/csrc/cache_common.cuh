@@ -211,6 +211,18 @@ bool make_tmap_codes(CUtensorMap *m, const void *base, int D, int page, long lon
 cudaError_t launch_fwd_join(const FwdParams &p, int dtype, cudaStream_t st);
 cudaError_t launch_weights(const FwdParams &p, cudaStream_t st);
 
+// A kernel's limit of dynamic shared memory, raised once per device.
+template <typename K> cudaError_t raise_smem(K kernel, std::atomic<unsigned long long> &done, size_t bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 struct AppendParams {
   View c;
   int S, span;  // span: pages that S tokens can touch

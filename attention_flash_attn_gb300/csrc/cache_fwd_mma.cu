@@ -650,18 +650,6 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
   }
 }
 
-// The kernel's shared-memory limit, raised once per device.
-template <typename K> cudaError_t raise_smem(K kernel, std::atomic<unsigned long long> &done, size_t bytes) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
-  if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-  return e;
-}
-
 template <int KIND, int D, int MT>
 cudaError_t launch_t(const FwdParams &p, cudaStream_t st) {
   using C = Cfg<D, MT>;
