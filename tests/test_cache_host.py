@@ -194,7 +194,7 @@ class HostCache(fa.AttnCache):
     def __init__(self):
         from attention_flash_attn_gb300._capi import AttnCacheArgs
         self.k, self.v, self.k_scale, self.v_scale = tensors()
-        self.page_size = 64
+        self.num_pages, self.Hkv, self.page_size, self.D, self.device = 4, 2, 64, 128, torch.device("cpu")
         self.status = torch.zeros(256, dtype=torch.uint8)
         self._c = AttnCacheArgs(1, 4, 64, 2, 128, FAKE, FAKE, FAKE, FAKE, FAKE)
         self._ref = ctypes.byref(self._c)
