@@ -211,6 +211,28 @@ bool make_tmap_codes(CUtensorMap *m, const void *base, int D, int page, long lon
 cudaError_t launch_fwd_join(const FwdParams &p, int dtype, cudaStream_t st);
 cudaError_t launch_weights(const FwdParams &p, cudaStream_t st);
 
+// Launches a kernel that may begin before the one ahead of it in the stream has ended (programmatic
+// dependent launch): it has to call grid_wait() before it touches anything of an earlier kernel, in every
+// block, so that what follows it is ordered behind both.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return counted(cudaLaunchKernelEx(&cfg, kernel, args...));
+}
+// Waits until the kernels ahead have ended and their writes are visible.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next kernel's blocks start (they wait above for this grid's end).
+__device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // A kernel's limit of dynamic shared memory, raised once per device.
 template <typename K> cudaError_t raise_smem(K kernel, std::atomic<unsigned long long> &done, size_t bytes) {
   int dev = 0;

@@ -188,6 +188,7 @@ template <int KIND, int NP>
 __global__ void __launch_bounds__(kMoveThr) cache_move_kernel(const __grid_constant__ EvictParams p) {
   __shared__ float s_m[kMoveThr / 32], s_scale[128];
   __shared__ long long s_row[128];  // first code of each row, or -1
+  grid_wait();
   const View &c = p.c;
   const int b = blockIdx.x / p.out_pages, nth = blockIdx.x - b * p.out_pages, h = blockIdx.y, t = threadIdx.x;
   const bool val = blockIdx.z == 1;
@@ -264,12 +265,11 @@ __global__ void __launch_bounds__(kMoveThr) cache_move_kernel(const __grid_const
 template <int KIND> cudaError_t launch_move(const EvictParams &p, cudaStream_t st) {
   const dim3 grid((unsigned)(p.c.B * p.out_pages), (unsigned)p.c.Hkv, 2);
   const int pieces = (p.c.page * (p.c.D / 16) + kMoveThr - 1) / kMoveThr;  // at most 16: pages of 128 by 512
-  if (pieces <= 1) cache_move_kernel<KIND, 1><<<grid, kMoveThr, 0, st>>>(p);
-  else if (pieces <= 2) cache_move_kernel<KIND, 2><<<grid, kMoveThr, 0, st>>>(p);
-  else if (pieces <= 4) cache_move_kernel<KIND, 4><<<grid, kMoveThr, 0, st>>>(p);
-  else if (pieces <= 8) cache_move_kernel<KIND, 8><<<grid, kMoveThr, 0, st>>>(p);
-  else cache_move_kernel<KIND, 16><<<grid, kMoveThr, 0, st>>>(p);
-  return counted(cudaGetLastError());
+  if (pieces <= 1) return launch_dependent(cache_move_kernel<KIND, 1>, grid, kMoveThr, 0, st, p);
+  if (pieces <= 2) return launch_dependent(cache_move_kernel<KIND, 2>, grid, kMoveThr, 0, st, p);
+  if (pieces <= 4) return launch_dependent(cache_move_kernel<KIND, 4>, grid, kMoveThr, 0, st, p);
+  if (pieces <= 8) return launch_dependent(cache_move_kernel<KIND, 8>, grid, kMoveThr, 0, st, p);
+  return launch_dependent(cache_move_kernel<KIND, 16>, grid, kMoveThr, 0, st, p);
 }
 
 }  // namespace

@@ -55,6 +55,7 @@ __global__ void __launch_bounds__(kThreads) cache_fwd_simt_kernel(const __grid_c
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   float *my_p = s_p + warp * kRows * 32;
 
+  grid_launch_next();  // (one wave of CTAs: the join's blocks take nobody's place)
   Cursor cur;
   if (!cursor_begin(p, cur)) return;
   Run run;
@@ -235,17 +236,21 @@ __global__ void __launch_bounds__(kThreads) cache_fwd_simt_kernel(const __grid_c
   }
 }
 
-// One block per row of an item that is split (or empty): the parts' outputs weighted by
-// 2^(M_c - M), four parts at a time (one per warp), and the extra column added once.
-template <typename T>
+// The rows of items that are split (or empty): the parts' outputs weighted by 2^(M_c - M), and the extra
+// column added once.  Bound by latency (prefix -> M, l -> O').  Many items have few parts each: a warp
+// per row (PER_ROW = 1 warp), four rows to a block; few items have many: a block per row, its warps
+// taking every fourth part.
+template <typename T, int PER_ROW>
 __global__ void __launch_bounds__(kThreads) cache_join_kernel(const __grid_constant__ FwdParams p) {
-  __shared__ float4 s_o[kWarps][128];
-  __shared__ float2 s_ml[kWarps];
-  const int hk = blockIdx.x / p.NG, g = blockIdx.x - hk * p.NG, b = g / p.RT, rt = g - b * p.RT;
-  const int r = rt * p.row_tile + blockIdx.y;
-  if (r >= p.R) return;
+  __shared__ float4 s_o[PER_ROW][PER_ROW > 1 ? 128 : 1];
+  __shared__ float2 s_ml[PER_ROW];
+  grid_wait();
+  grid_launch_next();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = p.c.D;
+  const int hk = blockIdx.x / p.NG, g = blockIdx.x - hk * p.NG, b = g / p.RT, rt = g - b * p.RT;
+  const int sub = PER_ROW > 1 ? (int)blockIdx.y : (int)blockIdx.y * kWarps + warp, r = rt * p.row_tile + sub;
   const int first = p.prefix[g], n = p.prefix[g + 1] - first, Uh = p.prefix[p.NG], s = hk * Uh + first;
+  if (sub >= p.row_tile || r >= p.R) return;
   const Shares sh(Uh * p.c.Hkv, p.max_ctas);
   int c0 = 0, c1 = -1;
   if (n > 0) {
@@ -256,19 +261,23 @@ __global__ void __launch_bounds__(kThreads) cache_join_kernel(const __grid_const
   // The row's partial of CTA c: the item is the second of the first CTA's two if it begins behind
   // that CTA's first unit, and the first of every later one's.
   const int second = n > 0 && s > sh.begin(c0) ? 1 : 0;
-  auto part = [&](int c) { return (size_t)(2 * c + (c == c0 ? second : 0)) * p.row_tile + blockIdx.y; };
+  auto part = [&](int c) { return (size_t)(2 * c + (c == c0 ? second : 0)) * p.row_tile + sub; };
+  const int me = PER_ROW > 1 ? warp : 0;
   float M = -CUDART_INF_F;
-  for (int c = c0 + threadIdx.x; c <= c1; c += kThreads) M = max_nan(M, p.ml_part[part(c)].x);
+  for (int c = c0 + me * 32 + lane; c <= c1; c += PER_ROW * 32) M = max_nan(M, p.ml_part[part(c)].x);
   M = warp_max(M);
-  if (lane == 0) s_ml[warp].x = M;
-  __syncthreads();
-  M = max_nan(max_nan(s_ml[0].x, s_ml[1].x), max_nan(s_ml[2].x, s_ml[3].x));
+  if (PER_ROW > 1) {
+    if (lane == 0) s_ml[warp].x = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < PER_ROW; ++w) M = max_nan(M, s_ml[w].x);
+  }
   float L = 0.f;
   float4 acc[4];  // 512 columns
 #pragma unroll
   for (int x = 0; x < 4; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int c = c0 + warp; c <= c1; c += kWarps) {
+  for (int c = c0 + me; c <= c1; c += PER_ROW) {
     const size_t at = part(c);
     const float2 ml = p.ml_part[at];
     if (ml.x == -CUDART_INF_F) continue;
@@ -283,31 +292,46 @@ __global__ void __launch_bounds__(kThreads) cache_join_kernel(const __grid_const
       }
     }
   }
-  if (lane == 0) s_ml[warp].y = L;
+  if (PER_ROW > 1) {
+    if (lane == 0) s_ml[warp].y = L;
 #pragma unroll
-  for (int x = 0; x < 4; ++x) s_o[warp][x * 32 + lane] = acc[x];
-  __syncthreads();
-  L = (s_ml[0].y + s_ml[1].y) + (s_ml[2].y + s_ml[3].y);
+    for (int x = 0; x < 4; ++x) s_o[warp][PER_ROW > 1 ? x * 32 + lane : 0] = acc[x];
+    __syncthreads();
+    L = 0.f;
+#pragma unroll
+    for (int w = 0; w < PER_ROW; ++w) L += s_ml[w].y;
+  }
   const RowEnd e = row_end(p, hk * p.G + r % p.G, M, L);
-  if (threadIdx.x == 0) p.LSE[lse_at(p, b, hk, r)] = e.lse;
-  const int d = threadIdx.x * 4;
-  if (d < D) {
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (M != -CUDART_INF_F) {
+  const bool none = M == -CUDART_INF_F;
+  T *out = static_cast<T *>(p.O) + o_row(p, b, hk, r);
+  if (PER_ROW > 1 ? threadIdx.x == 0 : lane == 0) p.LSE[lse_at(p, b, hk, r)] = e.lse;
+  auto put = [&](int d, float4 o) {
+    if (none) o = make_float4(0.f, 0.f, 0.f, 0.f);
+    o.x *= e.scale; o.y *= e.scale; o.z *= e.scale; o.w *= e.scale;
+    store4f(out + d, o);
+  };
+  if (PER_ROW > 1) {
+    const int d = threadIdx.x * 4;
+    if (d < D) {
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float4 v = s_o[w][threadIdx.x];
+      for (int w = 0; w < PER_ROW; ++w) {
+        const float4 v = s_o[w][PER_ROW > 1 ? threadIdx.x : 0];
         o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
       }
-      o.x *= e.scale; o.y *= e.scale; o.z *= e.scale; o.w *= e.scale;
+      put(d, o);
     }
-    store4f(static_cast<T *>(p.O) + o_row(p, b, hk, r) + d, o);
+  } else {
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (x * 128 + lane * 4 < D) put(x * 128 + lane * 4, acc[x]);
   }
 }
 
 // weights_out = weights + sum over the rows of 2^(score - LSE): four keys per thread, the rows'
 // scores read as the attention kernel stored them, summed in row order.
 __global__ void __launch_bounds__(kThreads) cache_weights_kernel(const __grid_constant__ FwdParams p) {
+  grid_wait();
   const int b = blockIdx.x / p.c.Hkv, hk = blockIdx.x - b * p.c.Hkv;
   const int len = seq_len(p.c, b);
   const int j0 = (blockIdx.y * kThreads + threadIdx.x) * 4;
@@ -358,20 +382,23 @@ cudaError_t launch_fwd_simt(const FwdParams &p, int dtype, int kind, cudaStream_
                                  : launch_simt_t<__nv_bfloat16, ATTN_CACHE_INT8>(p, st);
 }
 
+template <typename T> static cudaError_t launch_join_t(const FwdParams &p, cudaStream_t st) {
+  const int rows = min(p.row_tile, p.R);
+  const unsigned items = (unsigned)(p.NG * p.c.Hkv);
+  // Parts per item are at most 1 + CTAs / items on average.
+  if ((long long)items * 4 >= p.max_ctas)
+    return launch_dependent(cache_join_kernel<T, 1>, dim3(items, (rows + kWarps - 1) / kWarps), kThreads, 0, st, p);
+  return launch_dependent(cache_join_kernel<T, kWarps>, dim3(items, rows), kThreads, 0, st, p);
+}
+
 cudaError_t launch_fwd_join(const FwdParams &p, int dtype, cudaStream_t st) {
-  const dim3 grid((unsigned)(p.NG * p.c.Hkv), (unsigned)min(p.row_tile, p.R));
-  if (dtype == kF32)
-    cache_join_kernel<float><<<grid, kThreads, 0, st>>>(p);
-  else
-    cache_join_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(p);
-  return counted(cudaGetLastError());
+  return dtype == kF32 ? launch_join_t<float>(p, st) : launch_join_t<__nv_bfloat16>(p, st);
 }
 
 cudaError_t launch_weights(const FwdParams &p, cudaStream_t st) {
   const long long cap = (long long)p.c.max_pages << p.c.page_shift;
   const dim3 grid((unsigned)(p.c.B * p.c.Hkv), (unsigned)((cap + 4 * kThreads - 1) / (4 * kThreads)));
-  cache_weights_kernel<<<grid, kThreads, 0, st>>>(p);
-  return counted(cudaGetLastError());
+  return launch_dependent(cache_weights_kernel, grid, kThreads, 0, st, p);
 }
 
 }  // namespace cache

@@ -187,7 +187,10 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
   __syncwarp();
 
   Cursor cur;
-  if (!cursor_begin(p, cur)) return;
+  if (!cursor_begin(p, cur)) {
+    grid_launch_next();
+    return;
+  }
   Run run;
   uint32_t phases = 0;  // parity of each stage's next completion
   int stage = 0;
@@ -567,6 +570,8 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
       }
       stage = stage + 1 == C::DEPTH ? 0 : stage + 1;
     }
+
+    if (cur.u >= cur.u1) grid_launch_next();  // the join's blocks may take up their places
 
     // The run's end: each warp leaves its rows in its ring (nothing is in flight), four columns at a time,
     // the 16-byte groups permuted so that the lanes of a store meet different banks; then all threads add
