@@ -92,9 +92,9 @@ int validate(const attn_cache *c, const attn_cache_seqs *s, const attn_cache_fwd
   if (!strides_ok(a->dtype, {a->q_stride_b, a->q_stride_s, a->q_stride_h})) return ATTN_ERR_INVALID;
   const long long R = (long long)(a->Hq / c->Hkv) * a->Sq;
   // Positions of queries stay clear of 32 bits, the join's grid and the count of units
-  // (128 keys of a row tile of 8) within 31.
+  // (64 keys, at the least, of a row tile of 8) within 31.
   if (a->Sq > (1 << 24) || R > INT_MAX / 2) return ATTN_ERR_UNSUPPORTED;
-  const double units = (double)((R + 7) / 8) * s->B * c->Hkv * ((long long)s->max_pages * c->page_size / kUnit + 1);
+  const double units = (double)((R + 7) / 8) * s->B * c->Hkv * ((long long)s->max_pages * c->page_size / 64 + 1);
   if (units > INT_MAX) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
@@ -118,7 +118,8 @@ FwdParams fwd_params(const attn_cache *c, const attn_cache_seqs *s, const attn_c
   p.RT = (p.R + p.row_tile - 1) / p.row_tile;
   p.NG = s->B * p.RT;
   const long long cap = (long long)s->max_pages * c->page_size;
-  const long long most = std::max(1LL, (long long)p.NG * c->Hkv * ((cap + 31) / 32 * 32 + kUnit - 1) / kUnit);
+  p.unit_shift = mma ? mma_unit_shift(c->D) : simt_unit_shift();
+  const long long most = std::max(1LL, (long long)p.NG * c->Hkv * ((cap >> p.unit_shift) + 1));
   p.max_ctas = (int)std::min(most, (mma ? mma_ctas_per_sm(c->D, p.row_tile) : 4LL) * device_sm_count());
   p.causal = a->causal ? 1 : 0;
   p.window = a->window > 0 ? std::min(a->window, 1 << 30) : 0;  // (no sequence is longer)
@@ -135,7 +136,7 @@ FwdParams fwd_params(const attn_cache *c, const attn_cache_seqs *s, const attn_c
   p.w_out = a->weights_out;
   p.w_sb = a->weights_stride_b;
   p.w_sh = a->weights_stride_h;
-  p.Lpad = (cap + 31) / 32 * 32;
+  p.Lpad = (cap + 63) / 64 * 64;
   size_t off = 0;
   L->prefix = off; off += align_up(((size_t)p.NG + 1) * sizeof(int));
   L->o_part = off; off += align_up((size_t)2 * p.max_ctas * p.row_tile * c->D * sizeof(float));

@@ -138,6 +138,7 @@ struct FwdParams {
   int Sq, Hq, G, R;      // R = G * Sq: query rows of one (sequence, kv head); row r is query r / G,
                          // head h * G + r % G
   int row_tile, NG, RT;  // rows per work item; RT = ceil(R / row_tile); NG = B * RT groups (b, tile)
+  int unit_shift;        // keys of one unit of work: a slice for each warp of a CTA
   int max_ctas;
   int causal, window;
   float cap, inv_cap, scale;
@@ -158,10 +159,11 @@ struct FwdParams {
   long long Lpad;
 };
 
-constexpr int kUnit = 128;  // keys of one unit of work: four warps of 32
+// The query of row r (a division only where there is more than one).
+__device__ __forceinline__ int query_of(const FwdParams &p, int r) { return p.Sq == 1 ? 0 : r / p.G; }
 
-// The keys [lo, hi) that some row of a group's tile sees; lo rounded down to 32 keys (slices of a
-// warp start on multiples of 32, so that they lie in one page, or in whole pages of 16).
+// The keys [lo, hi) that some row of a group's tile sees; lo rounded down to 64 keys (the slices of a
+// warp, 16 to 64 keys, start on multiples of their size, so that they lie in one page or in whole pages).
 struct Range {
   int lo, hi, len;
 };
@@ -172,12 +174,12 @@ __device__ __forceinline__ Range group_range(const FwdParams &p, int b, int rt) 
   g.lo = 0;
   if (p.causal | (p.window > 0)) {
     const int r0 = rt * p.row_tile, r1 = min(p.R, r0 + p.row_tile) - 1, q0 = g.len - p.Sq;  // position of query 0
-    if (p.causal) g.hi = max(0, min(g.len, q0 + r1 / p.G + 1));
-    if (p.window > 0) g.lo = min(g.hi, max(0, q0 + r0 / p.G - p.window + 1) & ~31);
+    if (p.causal) g.hi = max(0, min(g.len, q0 + query_of(p, r1) + 1));
+    if (p.window > 0) g.lo = min(g.hi, max(0, q0 + query_of(p, r0) - p.window + 1) & ~63);
   }
   return g;
 }
-__device__ __forceinline__ int range_units(const Range &g) { return (g.hi - g.lo + kUnit - 1) / kUnit; }
+__device__ __forceinline__ int range_units(const FwdParams &p, const Range &g) { return (g.hi - g.lo + (1 << p.unit_shift) - 1) >> p.unit_shift; }
 
 // U units over at most max_ctas CTAs, as evenly as they go: the first `extra` CTAs have one more.
 struct Shares {
@@ -200,11 +202,13 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 cudaError_t launch_fwd_simt(const FwdParams &p, int dtype, int kind, cudaStream_t st);
 int simt_row_tile();
+int simt_unit_shift();
 
 // Tensor-core path.
 bool mma_supported(int dtype, int D);
 int mma_row_tile(int D, int R);
 int mma_ctas_per_sm(int D, int row_tile);
+int mma_unit_shift(int D);
 cudaError_t launch_fwd_mma(const FwdParams &p, int kind, cudaStream_t st);
 bool make_tmap_codes(CUtensorMap *m, const void *base, int D, int page, long long heads, int box_rows);
 

@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kThreads) cache_fwd_simt_kernel(const __grid_c
       const int r = x / (D / 4), d = (x - r * (D / 4)) * 4;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < rows) {
-        const int i = (r0 + r) / p.G, h = run.hk * p.G + (r0 + r - i * p.G);
+        const int i = query_of(p, r0 + r), h = run.hk * p.G + (r0 + r - i * p.G);
         v = load4f(static_cast<const T *>(p.q) + run.b * p.q_sb + i * p.q_ss + h * p.q_sh + d);
       }
       *reinterpret_cast<float4 *>(s_q + r * D + d) = v;
@@ -79,13 +79,13 @@ __global__ void __launch_bounds__(kThreads) cache_fwd_simt_kernel(const __grid_c
     for (int r = 0; r < kRows; ++r) {
       m[r] = -CUDART_INF_F;
       l[r] = 0.f;
-      see[r] = row_sees(p, run.range.len, (r0 + r) / p.G);
+      see[r] = row_sees(p, run.range.len, query_of(p, r0 + r));
 #pragma unroll
       for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int x = 0; x < 4; ++x) acc[r][c][x] = 0.f;
     }
-    const int key0 = run.range.lo + run.off * kUnit, key1 = min(run.range.hi, key0 + run.cnt * kUnit);
+    const int key0 = run.range.lo + (run.off << p.unit_shift), key1 = min(run.range.hi, key0 + (run.cnt << p.unit_shift));
     for (int base = key0 + warp * 32; base < key1; base += kWarps * 32) {
       const int pos = base + lane;
       int page = -1;
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreads) cache_weights_kernel(const __grid_co
   const float *row = scores_row(p, b, hk, 0) + j0;
   for (int r = 0; r < p.R; ++r, row += p.Lpad) {
     // Scores are stored for the keys that some row of the tile sees (a superset of these).
-    const int2 see = row_sees(p, len, r / p.G);
+    const int2 see = row_sees(p, len, query_of(p, r));
     if (j0 >= see.y || j0 + 3 < see.x) continue;
     const float lse2 = p.LSE[lse_at(p, b, hk, r)] * kLog2e;
     const float4 s = *reinterpret_cast<const float4 *>(row);
@@ -374,6 +374,7 @@ cudaError_t launch_simt_t(const FwdParams &p, cudaStream_t st) {
 }  // namespace
 
 int simt_row_tile() { return kRows; }
+int simt_unit_shift() { return 7; }  // four warps of 32 keys
 
 cudaError_t launch_fwd_simt(const FwdParams &p, int dtype, int kind, cudaStream_t st) {
   if (dtype == kF32)

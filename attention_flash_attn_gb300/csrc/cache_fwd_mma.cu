@@ -30,16 +30,17 @@ constexpr float kZeroLog = kMinScaleExp - 1;
 template <int D_, int MT_>
 struct Cfg {
   static constexpr int D = D_, MT = MT_;
-  static constexpr int SK = D == 256 ? 16 : 32;        // keys of a slice
-  static constexpr int NH = SK / 16;                   // 16-key halves: each lies in one page
+  static constexpr int SK = D == 256 ? 16 : D == 128 ? 32 : 64;  // keys of a slice: 8 KB of codes
+  static constexpr int NH = SK / 16;                   // groups of 16 keys: each lies in one page
   static constexpr int BLK = D < 128 ? D : 128;        // columns of one TMA box row
   static constexpr int NB = D / BLK;                   // boxes per row
   static constexpr int CH = BLK / 64;                  // 16-byte chunks per lane and key for Q K^T
   static constexpr int KS = D / 16;                    // k-steps of Q K^T
   static constexpr int NT = D / 8;                     // n-tiles of P V
+  static constexpr int QG = SK < 32 ? SK / 8 : 4;      // n-tiles of Q K^T whose codes are in registers at once
   static constexpr int STAGE = 2 * SK * D;             // bytes of a slice, K then V
-  static constexpr int DEPTH = D == 64 ? (MT == 1 ? 3 : 4) : 2;
-  static constexpr int CTAS = MT == 1 ? (D == 64 ? 4 : D == 128 ? 3 : 2) : 2;
+  static constexpr int DEPTH = 2;
+  static constexpr int CTAS = MT == 1 && D <= 128 ? 3 : 2;
   static constexpr bool QREG = D * MT <= 64;           // Q fragments in registers, else in shared memory
   static constexpr int ROWS = 16 * MT;
   static constexpr size_t RING = (size_t)kWarps * DEPTH * STAGE;
@@ -117,17 +118,18 @@ template <int BLK> __device__ __forceinline__ uint32_t swz(int row, int ch) {
 // Makes a slice's values fit to be multiplied by P where some row does not see every key: rows of
 // keys that no row sees (slots behind the last token may hold anything) become 0, and e4m3 NaNs too,
 // after the outputs that they belong to -- of the rows that see their key -- are marked in s_nan.  Only a
-// run's first and last slices come here, so it is kept small rather than fast: one key per lane.
+// run's first and last slices come here, so it is kept small rather than fast: a key per lane.
 template <int KIND, int D, int MT>
 __device__ __noinline__ void scrub_values(const FwdParams &p, uint32_t sv, int pos, int key1, unsigned gone, int len, int r0, int rows,
                                           uint32_t *s_nan, int *s_any) {
   using C = Cfg<D, MT>;
   const int lane = threadIdx.x & 31;
-  if (lane < C::SK) {
-    const bool hide = pos + lane >= key1 || ((gone >> (lane >> 4)) & 1u);
+#pragma unroll 1
+  for (int row = lane; row < C::SK; row += 32) {
+    const bool hide = pos + row >= key1 || ((gone >> (row >> 4)) & 1u);
 #pragma unroll 1
     for (int c = 0; c < D / 16; ++c) {
-      const uint32_t at = sv + (c * 16 / C::BLK) * (C::SK * C::BLK) + swz<C::BLK>(lane, c % (C::BLK / 16));
+      const uint32_t at = sv + (c * 16 / C::BLK) * (C::SK * C::BLK) + swz<C::BLK>(row, c % (C::BLK / 16));
       uint4 u = lds128(at);
       uint32_t w[4] = {u.x, u.y, u.z, u.w};
       bool write = hide;
@@ -141,7 +143,7 @@ __device__ __noinline__ void scrub_values(const FwdParams &p, uint32_t sv, int p
             write = true;
 #pragma unroll 1
             for (int r = 0; r < rows; ++r)
-              if (within(row_sees(p, len, (r0 + r) / p.G), pos + lane))
+              if (within(row_sees(p, len, query_of(p, r0 + r)), pos + row))
 #pragma unroll 1
                 for (int y = 0; y < 4; ++y)
                   if ((nan >> (8 * y)) & 1u) {
@@ -199,7 +201,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
 #pragma unroll 1
   while (cursor_next(p, cur, run)) {
     const int r0 = run.rt * C::ROWS, rows = min(C::ROWS, p.R - r0);
-    const int key0 = run.range.lo + run.off * kUnit, key1 = min(run.range.hi, key0 + run.cnt * kUnit);
+    const int key0 = run.range.lo + (run.off << p.unit_shift), key1 = min(run.range.hi, key0 + (run.cnt << p.unit_shift));
     // This warp's slices: key0 + (warp + 4 x) SK for x < n_slices.
     const int n_slices = (key1 - key0 - warp * C::SK + kWarps * C::SK - 1) / (kWarps * C::SK);  // <= 0: none
 
@@ -240,22 +242,22 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
 #pragma unroll
       for (int h = 0; h < C::NH; ++h) id[h] = __shfl_sync(~0u, ids[h], x & 31);
       if (lane == 0) {
-        const int pos = key0 + (warp + kWarps * x) * C::SK, slot = pos & (p.c.page - 1);
-        const bool two = C::NH == 2 && p.c.page == 16;  // the halves are pages of their own
+        const int pos = key0 + (warp + kWarps * x) * C::SK;
+        const int box = min(p.c.page, C::SK);  // rows of one load
         uint32_t bytes = 0;
-        if (!two) bytes = id[0] >= 0 ? C::STAGE : 0;
-        else bytes = (id[0] >= 0 ? C::STAGE / 2 : 0) + (id[C::NH - 1] >= 0 ? C::STAGE / 2 : 0);
+#pragma unroll
+        for (int h = 0; h < C::NH; ++h)
+          if (16 * h % box == 0 && id[h] >= 0) bytes += 2 * D * box;
         mbar_arrive_expect_tx(bar, bytes);
 #pragma unroll
         for (int h = 0; h < C::NH; ++h) {
-          if (h > 0 && !two) break;
-          if (id[h] < 0) continue;
+          if (16 * h % box != 0 || id[h] < 0) continue;
           const int head = id[h] * p.c.Hkv + run.hk;
 #pragma unroll
           for (int j = 0; j < C::NB; ++j) {
             const uint32_t to = dst + j * (C::SK * C::BLK) + h * (16 * C::BLK);
-            tma_load_3d(to, &kmap, bar, j * C::BLK, slot, head);
-            tma_load_3d(to + C::SK * D, &vmap, bar, j * C::BLK, slot, head);
+            tma_load_3d(to, &kmap, bar, j * C::BLK, (pos + 16 * h) & (p.c.page - 1), head);
+            tma_load_3d(to + C::SK * D, &vmap, bar, j * C::BLK, (pos + 16 * h) & (p.c.page - 1), head);
           }
         }
       }
@@ -279,7 +281,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int r = r0 + mt * 16 + 8 * y + g;
-        const int i = r / p.G, h = run.hk * p.G + (r - i * p.G);
+        const int i = query_of(p, r), h = run.hk * p.G + (r - i * p.G);
         const int2 see = row_sees(p, run.range.len, i);
         see_lo[mt][y] = see.x;
         see_n[mt][y] = max(0, min(see.y, key1) - see.x);
@@ -348,8 +350,8 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
         for (int x = 0; x < 4; ++x) o[mt][n][x] = 0.f;
     }
     // The keys that every row of the tile sees (rows' positions ascend).
-    const int all_from = row_sees(p, run.range.len, (r0 + rows - 1) / p.G).x;
-    const int all_below = min(key1, row_sees(p, run.range.len, r0 / p.G).y);
+    const int all_from = row_sees(p, run.range.len, query_of(p, r0 + rows - 1)).x;
+    const int all_below = min(key1, row_sees(p, run.range.len, query_of(p, r0)).y);
 
 #pragma unroll 1
     for (int x = 0; x < n_slices; ++x) {
@@ -383,35 +385,37 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
 #pragma unroll
         for (int j = 0; j < C::NB; ++j)
 #pragma unroll
-          for (int c = 0; c < C::CH; ++c) {
-            uint4 kw[C::SK / 8];
+          for (int c = 0; c < C::CH; ++c)
 #pragma unroll
-            for (int n = 0; n < C::SK / 8; ++n)
-              kw[n] = lds128(sk + j * (C::SK * C::BLK) + n * (8 * C::BLK) + swz<C::BLK>(g, t * C::CH + c));
+            for (int n0 = 0; n0 < C::SK / 8; n0 += C::QG) {
+              uint4 kw[C::QG];
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int step = (j * C::CH + c) * 4 + w;
-              uint4 qs[MT];
+              for (int n = 0; n < C::QG; ++n)
+                kw[n] = lds128(sk + j * (C::SK * C::BLK) + (n0 + n) * (8 * C::BLK) + swz<C::BLK>(g, t * C::CH + c));
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt)
-                if (!C::QREG) qs[mt] = s_q[(mt * C::KS + step) * 32 + lane];
+              for (int w = 0; w < 4; ++w) {
+                const int step = (j * C::CH + c) * 4 + w;
+                uint4 qs[MT];
 #pragma unroll
-              for (int n = 0; n < C::SK / 8; ++n) {
-                const uint32_t word = w == 0 ? kw[n].x : w == 1 ? kw[n].y : w == 2 ? kw[n].z : kw[n].w;
-                uint32_t b0, b1;
-                widen4<KIND>(word, b0, b1);
+                for (int mt = 0; mt < MT; ++mt)
+                  if (!C::QREG) qs[mt] = s_q[(mt * C::KS + step) * 32 + lane];
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                  if (C::QREG) {
-                    mma_f16(s[mt][n], qf[C::QREG ? mt : 0][C::QREG ? step : 0], b0, b1);
-                  } else {
-                    const uint32_t a[4] = {qs[mt].x, qs[mt].y, qs[mt].z, qs[mt].w};
-                    mma_f16(s[mt][n], a, b0, b1);
+                for (int n = 0; n < C::QG; ++n) {
+                  const uint32_t word = w == 0 ? kw[n].x : w == 1 ? kw[n].y : w == 2 ? kw[n].z : kw[n].w;
+                  uint32_t b0, b1;
+                  widen4<KIND>(word, b0, b1);
+#pragma unroll
+                  for (int mt = 0; mt < MT; ++mt) {
+                    if (C::QREG) {
+                      mma_f16(s[mt][n0 + n], qf[C::QREG ? mt : 0][C::QREG ? step : 0], b0, b1);
+                    } else {
+                      const uint32_t a[4] = {qs[mt].x, qs[mt].y, qs[mt].z, qs[mt].w};
+                      mma_f16(s[mt][n0 + n], a, b0, b1);
+                    }
                   }
                 }
               }
             }
-          }
         // Softmax.  A probability is 2^(f s + lv - m): f takes a raw score to a logit in base 2 (it is not
         // negative, so that the largest raw score gives the largest logit), lv is the values' scale.  With a cap
         // or a mask the logits are formed first, and f is 1.
@@ -502,6 +506,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
               const float a = mn[mt][y] == -CUDART_INF_F ? 1.f : ex2(m[mt][y] - mn[mt][y]);
               m[mt][y] = mn[mt][y];
               l[mt][y] *= a;
+              if (x == 0) continue;  // nothing there yet
 #pragma unroll
               for (int n = 0; n < C::NT; ++n) {
                 o[mt][n][2 * y] *= a;
@@ -688,8 +693,10 @@ bool mma_supported(int dtype, int D) { return dtype == kBF16 && (D == 64 || D ==
 // (head dims up to 128), so that widening a code serves two row tiles.
 int mma_row_tile(int D, int R) { return R > 16 && D <= 128 ? 32 : 16; }
 
+int mma_unit_shift(int D) { return D == 64 ? 8 : D == 128 ? 7 : 6; }  // four slices
+
 int mma_ctas_per_sm(int D, int row_tile) {
-  return row_tile == 32 ? 2 : D == 64 ? Cfg<64, 1>::CTAS : D == 128 ? Cfg<128, 1>::CTAS : Cfg<256, 1>::CTAS;
+  return row_tile == 32 || D == 256 ? 2 : 3;  // Cfg's CTAS
 }
 
 cudaError_t launch_fwd_mma(const FwdParams &p, int kind, cudaStream_t st) {

@@ -1,5 +1,5 @@
 // cache_work.cuh -- how attention over the cache is spread over the grid, and how a piece of work
-// ends.  Work items are (kv head, sequence, row tile); an item's keys are cut into units of 128,
+// ends.  Work items are (kv head, sequence, row tile); an item's keys are cut into units (a slice for each warp),
 // and the units of all items, in that order, are shared out evenly over the CTAs: one long
 // sequence is split over the whole grid, many short ones are run several to a CTA, and ragged
 // batches balance.  A CTA turns each run of units of one item into either the item's result, if
@@ -36,7 +36,7 @@ struct Run {
 
 __device__ __forceinline__ int group_units(const FwdParams &p, int g) {
   const int b = p.RT == 1 ? g : g / p.RT;
-  return range_units(group_range(p, b, g - b * p.RT));
+  return range_units(p, group_range(p, b, g - b * p.RT));
 }
 
 // Called by all kThreads threads; false if this CTA has no units.  CTA 0 stores the prefix sums and
@@ -109,7 +109,7 @@ __device__ __forceinline__ bool cursor_next(const FwdParams &p, Cursor &cur, Run
     run.b = p.RT == 1 ? cur.g : cur.g / p.RT;
     run.rt = cur.g - run.b * p.RT;
     run.range = group_range(p, run.b, run.rt);
-    run.n = range_units(run.range);
+    run.n = range_units(p, run.range);
     if (cur.u < cur.g_first + run.n) break;
     cur.g_first += run.n;
     if (++cur.g == p.NG) {
@@ -167,11 +167,11 @@ __device__ __forceinline__ RowEnd row_end(const FwdParams &p, int h, float M, fl
 
 // Where row r of an item lives in O (first element) and in LSE.
 __device__ __forceinline__ size_t o_row(const FwdParams &p, int b, int hk, int r) {
-  const int i = r / p.G, h = hk * p.G + (r - i * p.G);
+  const int i = query_of(p, r), h = hk * p.G + (r - i * p.G);
   return (((size_t)b * p.Sq + i) * p.Hq + h) * p.c.D;
 }
 __device__ __forceinline__ size_t lse_at(const FwdParams &p, int b, int hk, int r) {
-  const int i = r / p.G, h = hk * p.G + (r - i * p.G);
+  const int i = query_of(p, r), h = hk * p.G + (r - i * p.G);
   return ((size_t)b * p.Hq + h) * p.Sq + i;
 }
 __device__ __forceinline__ float *scores_row(const FwdParams &p, int b, int hk, int r) {
