@@ -3,7 +3,8 @@
 Every translation unit is compiled in parallel (one nvcc process each) into ``_build/``
 and linked into ``attention_flash_attn_gb300/libattn_gb300.so`` with the CUDA runtime
 linked statically, so the library loads without a GPU or a driver (the driver entry
-points it needs are resolved at run time).
+points it needs are resolved at run time).  csrc/binding.cpp, the calls that cache.py makes, is
+compiled with g++ against PyTorch's headers into ``_binding.so`` beside it.
 """
 from __future__ import annotations
 
@@ -13,12 +14,18 @@ import hashlib
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
+
+import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libattn_gb300.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
          "--expt-relaxed-constexpr"]
@@ -43,7 +50,9 @@ def _stamp() -> str:
         h.update(os.path.relpath(f, ROOT).encode())  # relative: the same sources hash alike anywhere
         with open(f, "rb") as fh:
             h.update(fh.read())
-    h.update(" ".join(ARCH + FLAGS).encode())
+    with open(BINDING_SRC, "rb") as fh:
+        h.update(fh.read())
+    h.update(" ".join(ARCH + FLAGS + [torch.__version__, sys.version]).encode())
     return h.hexdigest()
 
 
@@ -90,12 +99,35 @@ def kernel_stamp(names=BWD_MAIN_SOURCES) -> str:
     return h.hexdigest()
 
 
+def _compile_binding(out: str) -> None:
+    """g++ of csrc/binding.cpp against the PyTorch that runs this (its headers' directory, its libraries)."""
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include"), sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-c", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[x for i in inc for x in ("-isystem", i)], BINDING_SRC, "-o", out]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+
+
+def _link_binding(obj: str) -> None:
+    tmp = BINDING + f".tmp{os.getpid()}"
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libattn_gb300.so", "-Wl,-rpath,$ORIGIN", "-L", lib, "-ltorch_python",
+           "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile (if sources changed) and return the path of the shared library."""
     os.makedirs(BUILD, exist_ok=True)
     stamp_file = os.path.join(BUILD, "stamp")
     stamp = _stamp()
-    if not force and os.path.exists(LIB) and os.path.exists(stamp_file):
+    if not force and os.path.exists(LIB) and os.path.exists(BINDING) and os.path.exists(stamp_file):
         if open(stamp_file).read() == stamp:
             return LIB
     nvcc = _nvcc()
@@ -109,8 +141,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    binding_obj = os.path.join(BUILD, "binding.o")
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        binding = ex.submit(_compile_binding, binding_obj)
         results = list(ex.map(compile_one, srcs))
+        binding.result()
     log = "\n".join(err for _, err in results)
     with open(os.path.join(BUILD, "ptxas.log"), "w") as fh:
         fh.write(log)
@@ -122,6 +157,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     with open(stamp_file, "w") as fh:
         fh.write(stamp)
     return LIB

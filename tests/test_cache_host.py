@@ -197,7 +197,7 @@ class HostCache(fa.AttnCache):
         self.num_pages, self.Hkv, self.page_size, self.D, self.device = 4, 2, 64, 128, torch.device("cpu")
         self.status = torch.zeros(256, dtype=torch.uint8)
         self._c = AttnCacheArgs(1, 4, 64, 2, 128, FAKE, FAKE, FAKE, FAKE, FAKE)
-        self._ref = ctypes.byref(self._c)
+        self._addr = ctypes.addressof(self._c)
 
 
 def ints(*x):
