@@ -1,9 +1,11 @@
 // cache_append.cu -- quantisation of new tokens into the paged 8-bit cache.
 //
-// One block per (sequence, page the new tokens touch, kv head, K or V).  The new rows' largest
-// magnitude gives the scale they need, the least power of two; a page that holds earlier tokens
-// keeps the larger of that and its present scale, and when it grows, the earlier codes are moved to
-// it.  Bound by reading the new rows (2 or 4 bytes a value) and writing codes (1 byte).
+// The new rows' largest magnitude gives the scale they need, the least power of two; a page that holds
+// earlier tokens keeps the larger of that and its present scale, and when it grows, the earlier codes are
+// moved to it.  Prompts: one block per (sequence, page the new tokens touch, kv head, K or V), which
+// reads its rows once, into registers (what does not fit there it reads again, from L2).  Single tokens: one warp each.  Bound by reading the new rows (2 or
+// 4 bytes a value) and writing codes (1 byte); a step of single tokens by the chain length -> page ->
+// scale.
 #include "cache_common.cuh"
 
 namespace attn {
@@ -11,40 +13,127 @@ namespace cache {
 namespace {
 
 constexpr int kThr = 256;
+constexpr int kHeld = 4;  // pieces of 8 values that a thread keeps between the two looks at them
 
-template <typename T> __device__ __forceinline__ void load8(const T *p, float *x);
-template <> __device__ __forceinline__ void load8<float>(const float *p, float *x) {
-  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-template <> __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, float *x) {
-  const uint4 u = *reinterpret_cast<const uint4 *>(p);
-  const unsigned w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// Eight values as they lie in memory, as floats, and their largest magnitude (NaN if one is NaN).
+template <typename T> struct Raw;
+template <> struct Raw<float> {
+  uint4 a, b;
+  __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void load(const float *p) {
+    a = reinterpret_cast<const uint4 *>(p)[0];
+    b = reinterpret_cast<const uint4 *>(p)[1];
   }
-}
+  __device__ __forceinline__ void get(float *x) const {
+    const unsigned w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+  }
+  __device__ __forceinline__ float amax() const {
+    float x[8], m = 0.f;
+    get(x);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) m = max_nan(m, fabsf(x[i]), fabsf(x[i + 1]));
+    return m;
+  }
+};
+template <> struct Raw<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = *reinterpret_cast<const uint4 *>(p); }
+  __device__ __forceinline__ void get(float *x) const {
+    const unsigned w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ float amax() const {
+    const unsigned w[4] = {a.x, a.y, a.z, a.w};
+    __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[0]));
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i])));
+    return max_nan(__low2float(m), __high2float(m));
+  }
+};
 
-template <int KIND> __device__ __forceinline__ uint2 encode8(const float *x, float inv) {
+// Codes of 8 values in units of 1 / inv.  FIT: they are known to be finite and within the largest code.
+template <int KIND, bool FIT> __device__ __forceinline__ uint2 encode8(const float *x, float inv) {
   uint2 o;
-  o.x = encode2<KIND>(x[0] * inv, x[1] * inv) | (encode2<KIND>(x[2] * inv, x[3] * inv) << 16);
-  o.y = encode2<KIND>(x[4] * inv, x[5] * inv) | (encode2<KIND>(x[6] * inv, x[7] * inv) << 16);
+  if (KIND == ATTN_CACHE_INT8 && FIT) {
+    unsigned u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(fmaf(x[i], inv, 12582912.f));  // rounded once, to an integer
+    o.x = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+    o.y = __byte_perm(__byte_perm(u[4], u[5], 0x0040), __byte_perm(u[6], u[7], 0x0040), 0x5410);
+  } else {
+    o.x = encode2<KIND>(x[0] * inv, x[1] * inv) | (encode2<KIND>(x[2] * inv, x[3] * inv) << 16);
+    o.y = encode2<KIND>(x[4] * inv, x[5] * inv) | (encode2<KIND>(x[6] * inv, x[7] * inv) << 16);
+  }
   return o;
 }
 
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x = max_nan(x, __shfl_xor_sync(~0u, x, o));
+  return x;
+}
 // Maximum over the block; every thread gets it.
 __device__ __forceinline__ float block_max(float x) {
   __shared__ float s_m[kThr / 32];
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
+  x = warp_max(x);
+  __syncthreads();
   if ((threadIdx.x & 31) == 0) s_m[threadIdx.x >> 5] = x;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kThr / 32; ++w) x = fmaxf(x, s_m[w]);
+  for (int w = 0; w < kThr / 32; ++w) x = max_nan(x, s_m[w]);
   return x;
+}
+
+// Where a sequence's new tokens go: positions [len, end).  Writes the new length and records what is
+// out of place, once per sequence.
+struct Span {
+  int len, end;
+};
+__device__ __forceinline__ Span new_span(const AppendParams &p, int b, bool once) {
+  bool bad;
+  Span s;
+  s.len = seq_len(p.c, b, &bad);
+  int cnt = p.counts ? p.counts[b] : p.S;
+  cnt = cnt < 0 ? 0 : min(cnt, p.S);
+  const long long want = s.len + (long long)cnt, cap = (long long)p.c.max_pages << p.c.page_shift;
+  s.end = (int)(want > cap ? cap : want);
+  if (once) {
+    if (p.lengths_out) p.lengths_out[b] = s.end;
+    if (bad || s.end < want) set_status(p.c.status, kStatusBadPage);
+  }
+  return s;
+}
+
+constexpr float kMaxFloat = 3.402823466e38f;
+// Largest finite magnitude of 8 values.
+__device__ __forceinline__ float amax_finite(const float *v, float amax) {
+#pragma unroll
+  for (int y = 0; y < 8; ++y)
+    if (fabsf(v[y]) <= kMaxFloat) amax = fmaxf(amax, fabsf(v[y]));
+  return amax;
+}
+
+// Moves n16 pieces of 16 codes to a scale 1 / f times as large; called by `threads` threads.
+template <int KIND> __device__ __forceinline__ void rescale(uint4 *at, int n16, float f, int t, int threads) {
+#pragma unroll 4
+  for (int x = t; x < n16; x += threads) {
+    const uint4 w = at[x];
+    unsigned u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      float v[4];
+      decode4<KIND>(u[y], v);
+      u[y] = encode2<KIND>(v[0] * f, v[1] * f) | (encode2<KIND>(v[2] * f, v[3] * f) << 16);
+    }
+    at[x] = make_uint4(u[0], u[1], u[2], u[3]);
+  }
 }
 
 template <typename T, int KIND>
@@ -52,81 +141,139 @@ __global__ void __launch_bounds__(kThr) cache_append_kernel(const __grid_constan
   const View &c = p.c;
   const int b = blockIdx.x / p.span, nth = blockIdx.x - b * p.span, h = blockIdx.y, t = threadIdx.x;
   const bool val = blockIdx.z == 1;
-  bool bad;
-  const int len = seq_len(c, b, &bad);
-  int cnt = p.counts ? p.counts[b] : p.S;
-  cnt = cnt < 0 ? 0 : min(cnt, p.S);
-  const long long cap = (long long)c.max_pages << c.page_shift;
-  const int end = (int)(len + (long long)cnt > cap ? cap : len + (long long)cnt);  // positions [len, end) get a token
-  if (nth == 0 && h == 0 && !val && t == 0) {
-    if (p.lengths_out) p.lengths_out[b] = end;
-    if (bad || end < len + (long long)cnt) set_status(c.status, kStatusBadPage);
-  }
-  const int slot_page = (len >> c.page_shift) + nth;     // column of the table
-  const int first = max(len, slot_page << c.page_shift);  // the page's new positions: [first, last)
-  const int last = min((long long)end, ((long long)slot_page + 1) << c.page_shift);
+  const Span sp = new_span(p, b, nth == 0 && h == 0 && !val && t == 0);
+  const int len = sp.len, col = (len >> c.page_shift) + nth;  // column of the table
+  const int first = max(len, col << c.page_shift);            // the page's new positions: [first, last)
+  const int last = min((long long)sp.end, ((long long)col + 1) << c.page_shift);
   if (first >= last) return;
+  const int D = c.D, per = D / 8, total = (last - first) * per, old = first & (c.page - 1);
+  const long long ss = val ? p.v_ss : p.k_ss;
+  const T *src = static_cast<const T *>(val ? p.v : p.k) + b * (val ? p.v_sb : p.k_sb) + h * (val ? p.v_sh : p.k_sh) + (first - len) * ss;
+  auto at = [&](int i) {
+    const int r = i / per;
+    return src + r * ss + (i - r * per) * 8;
+  };
+  Raw<T> held[kHeld];
+#pragma unroll
+  for (int x = 0; x < kHeld; ++x) {
+    held[x].zero();
+    if (t + x * kThr < total) held[x].load(at(t + x * kThr));
+  }
   const int page = page_of(c, b, first);
   if (!val && p.weights)
     for (int x = first + t; x < last; x += kThr) p.weights[b * p.w_sb + h * p.w_sh + x] = 0.f;
   if (page < 0) return;
-  const int D = c.D, per = D / 8, fresh = last - first, old = first & (c.page - 1);
-  const T *src = static_cast<const T *>(val ? p.v : p.k) + b * (val ? p.v_sb : p.k_sb) + h * (val ? p.v_sh : p.k_sh);
-  const long long ss = val ? p.v_ss : p.k_ss;
   uint8_t *dst = (val ? c.v : c.k) + row_at(c, page, h, 0);
   float *sc = (val ? c.v_scale : c.k_scale) + (size_t)page * c.Hkv + h;
-
-  float amax = 0.f;
-  bool odd = false;
-  for (int x = t; x < fresh * per; x += kThr) {
-    const int r = x / per, d = (x - r * per) * 8;
-    float v[8];
-    load8(src + (first - len + r) * ss + d, v);
-#pragma unroll
-    for (int y = 0; y < 8; ++y) {
-      const float a = fabsf(v[y]);
-      if (a <= 3.402823466e38f) amax = fmaxf(amax, a);
-      else odd = true;
-    }
-  }
-  if (odd) set_status(c.status, kStatusNonFinite);
   const float was = *sc;
+  float amax = 0.f;
+#pragma unroll
+  for (int x = 0; x < kHeld; ++x) amax = max_nan(amax, held[x].amax());
+#pragma unroll 1
+  for (int i = t + kHeld * kThr; i < total; i += kThr) {  // pages of more than 8192 values
+    Raw<T> v;
+    v.load(at(i));
+    amax = max_nan(amax, v.amax());
+  }
   amax = block_max(amax);  // (and every thread has read the old scale)
+  const bool fit = amax <= kMaxFloat;
+  if (!fit) {  // something is infinite or NaN: the scale goes by the rest
+    if (t == 0) set_status(c.status, kStatusNonFinite);
+    amax = 0.f;
+#pragma unroll 1
+    for (int i = t; i < total; i += kThr) {
+      Raw<T> v;
+      v.load(at(i));
+      float x[8];
+      v.get(x);
+      amax = amax_finite(x, amax);
+    }
+    amax = block_max(amax);
+  }
   float s = need_scale<KIND>(amax);
   if (old > 0 && was >= s) s = was;
   const float inv = 1.f / s;  // exact for the powers of two that this library writes
-  for (int x = t; x < fresh * per; x += kThr) {
-    const int r = x / per, d = (x - r * per) * 8;
-    float v[8];
-    load8(src + (first - len + r) * ss + d, v);
-    *reinterpret_cast<uint2 *>(dst + (size_t)(old + r) * D + d) = encode8<KIND>(v, inv);
+  uint2 *to = reinterpret_cast<uint2 *>(dst + (size_t)old * D);
+  auto put = [&](int i, const Raw<T> &v) {
+    float x[8];
+    v.get(x);
+    to[i] = fit ? encode8<KIND, true>(x, inv) : encode8<KIND, false>(x, inv);
+  };
+#pragma unroll
+  for (int x = 0; x < kHeld; ++x)
+    if (t + x * kThr < total) put(t + x * kThr, held[x]);
+#pragma unroll 1
+  for (int i = t + kHeld * kThr; i < total; i += kThr) {
+    Raw<T> v;
+    v.load(at(i));
+    put(i, v);
   }
-  if (old > 0 && s != was) {
-    const float f = was * inv;
-    for (int x = t; x < old * per; x += kThr) {
-      uint2 *at = reinterpret_cast<uint2 *>(dst) + x;
-      const uint2 w = *at;
-      float v[8];
-      decode4<KIND>(w.x, v);
-      decode4<KIND>(w.y, v + 4);
-      *at = encode8<KIND>(v, f);
-    }
-  }
+  if (old > 0 && s != was) rescale<KIND>(reinterpret_cast<uint4 *>(dst), old * (D / 16), was * inv, t, kThr);
   if (t == 0) *sc = s;
+}
+
+// S = 1: warp w of the grid has (sequence, kv head, K or V).  The row is fetched before the chain that
+// says where it goes.
+template <typename T, int KIND>
+__global__ void __launch_bounds__(128) cache_append_token_kernel(const __grid_constant__ AppendParams p) {
+  const View &c = p.c;
+  const int task = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int b = task / (2 * c.Hkv), h = (task >> 1) - b * c.Hkv;
+  if (b >= c.B) return;
+  const bool val = task & 1;
+  const int D = c.D, per = D / 8;
+  const T *src = static_cast<const T *>(val ? p.v : p.k) + b * (val ? p.v_sb : p.k_sb) + h * (val ? p.v_sh : p.k_sh);
+  Raw<T> v[2];  // D <= 512: at most two pieces a lane
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v[i].zero();
+    if (lane + 32 * i < per) v[i].load(src + (lane + 32 * i) * 8);
+  }
+  const Span sp = new_span(p, b, h == 0 && !val && lane == 0);
+  if (sp.end <= sp.len) return;
+  const int page = page_of(c, b, sp.len), old = sp.len & (c.page - 1);
+  if (!val && p.weights && lane == 0) p.weights[b * p.w_sb + h * p.w_sh + sp.len] = 0.f;
+  if (page < 0) return;
+  uint8_t *dst = (val ? c.v : c.k) + row_at(c, page, h, 0);
+  float *sc = (val ? c.v_scale : c.k_scale) + (size_t)page * c.Hkv + h;
+  const float was = *sc;
+  float amax = warp_max(max_nan(v[0].amax(), v[1].amax()));
+  float x[2][8];
+  v[0].get(x[0]);
+  v[1].get(x[1]);
+  const bool fit = amax <= kMaxFloat;
+  if (!fit) {
+    if (lane == 0) set_status(c.status, kStatusNonFinite);
+    amax = warp_max(amax_finite(x[1], amax_finite(x[0], 0.f)));
+  }
+  float s = need_scale<KIND>(amax);
+  if (old > 0 && was >= s) s = was;
+  const float inv = 1.f / s;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (lane + 32 * i < per)
+      reinterpret_cast<uint2 *>(dst + (size_t)old * D)[lane + 32 * i] = fit ? encode8<KIND, true>(x[i], inv) : encode8<KIND, false>(x[i], inv);
+  if (old > 0 && s != was) rescale<KIND>(reinterpret_cast<uint4 *>(dst), old * (D / 16), was * inv, lane, 32);
+  if (lane == 0) *sc = s;
+}
+
+template <typename T, int KIND> cudaError_t launch_append_t(const AppendParams &p, cudaStream_t st) {
+  if (p.S == 1) {
+    const long long tasks = 2LL * p.c.B * p.c.Hkv;
+    cache_append_token_kernel<T, KIND><<<(unsigned)((tasks + 3) / 4), 128, 0, st>>>(p);
+  } else {
+    cache_append_kernel<T, KIND><<<dim3((unsigned)(p.c.B * p.span), (unsigned)p.c.Hkv, 2), kThr, 0, st>>>(p);
+  }
+  return counted(cudaGetLastError());
 }
 
 }  // namespace
 
 cudaError_t launch_append(const AppendParams &p, int dtype, int kind, cudaStream_t st) {
-  const dim3 grid((unsigned)(p.c.B * p.span), (unsigned)p.c.Hkv, 2);
-  if (dtype == kF32) {
-    if (kind == ATTN_CACHE_E4M3) cache_append_kernel<float, ATTN_CACHE_E4M3><<<grid, kThr, 0, st>>>(p);
-    else cache_append_kernel<float, ATTN_CACHE_INT8><<<grid, kThr, 0, st>>>(p);
-  } else {
-    if (kind == ATTN_CACHE_E4M3) cache_append_kernel<__nv_bfloat16, ATTN_CACHE_E4M3><<<grid, kThr, 0, st>>>(p);
-    else cache_append_kernel<__nv_bfloat16, ATTN_CACHE_INT8><<<grid, kThr, 0, st>>>(p);
-  }
-  return counted(cudaGetLastError());
+  if (dtype == kF32)
+    return kind == ATTN_CACHE_E4M3 ? launch_append_t<float, ATTN_CACHE_E4M3>(p, st) : launch_append_t<float, ATTN_CACHE_INT8>(p, st);
+  return kind == ATTN_CACHE_E4M3 ? launch_append_t<__nv_bfloat16, ATTN_CACHE_E4M3>(p, st)
+                                 : launch_append_t<__nv_bfloat16, ATTN_CACHE_INT8>(p, st);
 }
 
 }  // namespace cache

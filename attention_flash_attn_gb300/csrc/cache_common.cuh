@@ -85,36 +85,25 @@ template <int KIND> __device__ __forceinline__ unsigned encode2(float lo, float 
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
   }
-  const int a = lo == lo ? __float2int_rn(fminf(fmaxf(lo, -127.f), 127.f)) : 0;
-  const int b = hi == hi ? __float2int_rn(fminf(fmaxf(hi, -127.f), 127.f)) : 0;
-  return (a & 0xff) | ((b & 0xff) << 8);
+  // Adding 1.5 * 2^23 leaves the rounded integer in the low bits (a conversion would go to a slower unit).
+  const float a = fminf(fmaxf(lo == lo ? lo : 0.f, -127.f), 127.f) + 12582912.f;
+  const float b = fminf(fmaxf(hi == hi ? hi : 0.f, -127.f), 127.f) + 12582912.f;
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040) & 0xffffu;
 }
 
-// Two codes widened to fp16: exact for both kinds (e4m3 has fewer bits and a smaller range, int8
-// has 8 bits).
-template <int KIND> __device__ __forceinline__ unsigned decode2_h(unsigned codes) {
-  unsigned r;
-  if (KIND == ATTN_CACHE_E4M3) {
-    asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(r) : "r"(codes));
-  } else {
-    const __half2 h = __halves2half2(__int2half_rn((int)(signed char)(codes & 0xff)),
-                                     __int2half_rn((int)(signed char)((codes >> 8) & 0xff)));
-    r = *reinterpret_cast<const unsigned *>(&h);
-  }
-  return r;
-}
-template <int KIND> __device__ __forceinline__ float2 decode2(unsigned codes) {
-  const unsigned h = decode2_h<KIND>(codes);
-  return __half22float2(*reinterpret_cast<const __half2 *>(&h));
-}
-// Four codes of a word.
+// Four codes of a word as floats.  e4m3 by way of fp16, which holds it exactly; int8: code + 128 under
+// the bits of 2^23, less 2^23 + 128.
 template <int KIND> __device__ __forceinline__ void decode4(unsigned w, float *x) {
   if (KIND == ATTN_CACHE_E4M3) {
-    const float2 a = decode2<KIND>(w & 0xffffu), b = decode2<KIND>(w >> 16);
+    unsigned lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(w));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo)), b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
     x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
   } else {
+    const unsigned u = w ^ 0x80808080u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = (float)(int)(signed char)(w >> (8 * i));
+    for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7540 + i)) - 8388736.f;
   }
 }
 

@@ -11,6 +11,8 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kSelThr = 512, kSelWarps = kSelThr / 32;
+constexpr int kBins = 2048, kGroup = kBins / 32;  // counts of a digit; each lane of a warp has a group of them
+static_assert(kBins / kSelThr == 4 && kGroup == 64, "a group's counts are summed by 16 threads, four each");
 constexpr int kMoveThr = 256;
 constexpr int kSelSmemKeys = 49152;  // most weights that one CTA holds in shared memory (192 KB)
 
@@ -21,17 +23,26 @@ __device__ __forceinline__ unsigned order_of(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+__device__ __forceinline__ int warp_prefix(int x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(~0u, x, o);
+    if (lane >= o) x += v;
+  }
+  return x;
+}
+
 // One cluster per (sequence, kv head); each of its CTAs has a contiguous part of the middle positions
-// [first, n - recent), whose weights it reads once and keeps in shared memory in their integer order
-// (parts that do not fit are read again in every pass).  The K-th largest order T is found byte by byte:
-// each CTA counts the next byte of its weights that share the bytes found so far, and every CTA adds
-// up the cluster's counts through distributed shared memory.  Then every position above T stays, and
+// [first, n - recent), whose weights it reads once and keeps in shared memory
+// (parts that do not fit are read again in every pass).  The K-th largest order T is found in three
+// digits of 11, 11 and 10 bits: each CTA counts the next digit of its weights that share those found, and the
+// cluster's counts are added up through distributed shared memory.  Then every position above T stays, and
 // of those equal to T the lowest ones: each warp has a contiguous part, placed by prefix sums over the
-// warps' and the CTAs' counts, so that the result is ascending.  Lanes that count the same byte add once
-// (weights share few exponents).  Bound by latency: five cluster barriers and passes over shared memory.
+// warps' and the CTAs' counts, so that the result is ascending.  Bound by latency: four cluster barriers and passes over shared
+// memory.
 __global__ void __launch_bounds__(kSelThr) cache_select_kernel(const __grid_constant__ EvictParams p, int in_smem) {
-  extern __shared__ unsigned s_key[];
-  __shared__ unsigned s_hist[2][256], s_sum[256];
+  extern __shared__ float s_w[];
+  __shared__ unsigned s_hist[2][kBins], s_group[2][32];
   __shared__ int s_gt[kSelWarps], s_eq[kSelWarps], s_all[2], s_found[2];
   const cg::cluster_group cluster = cg::this_cluster();
   const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
@@ -71,59 +82,60 @@ __global__ void __launch_bounds__(kSelThr) cache_select_kernel(const __grid_cons
   const int a0 = min(hi, lo + rank * part), cnt = min(hi, a0 + part) - a0;
   const float *wp = w + a0;
   if (in_smem) {
-#pragma unroll 4
-    for (int i = t; i < cnt; i += kSelThr) s_key[i] = order_of(wp[i]);
+#pragma unroll 16
+    for (int i = t; i < cnt; i += kSelThr) s_w[i] = wp[i];
   }
-  for (int i = t; i < 512; i += kSelThr) s_hist[0][i] = 0;
+  for (int i = t; i < kBins; i += kSelThr) s_hist[0][i] = 0;
   __syncthreads();
-  auto key = [&](int i) { return in_smem ? s_key[i] : order_of(wp[i]); };
+  auto weight = [&](int i) { return in_smem ? s_w[i] : wp[i]; };
+  auto key = [&](int i) { return order_of(weight(i)); };
   unsigned prefix = 0;
   int want = K;
 #pragma unroll 1
-  for (int pass = 0; pass < 4; ++pass) {
-    const int shift = 24 - 8 * pass;
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
     unsigned *hist = s_hist[pass & 1];
-    for (int i0 = warp * 32; i0 < cnt; i0 += kSelThr) {
-      const int i = i0 + lane;
-      const unsigned u = i < cnt ? key(i) : 0u;
-      const bool in = i < cnt && (pass == 0 || (u >> (shift + 8)) == prefix);
-      const unsigned digit = (u >> shift) & 255u;
-      const unsigned same = __match_any_sync(~0u, in ? digit : 256u);
-      if (in && (same & ((1u << lane) - 1)) == 0) atomicAdd(&hist[digit], __popc(same));
+#pragma unroll 4
+    for (int i = t; i < cnt; i += kSelThr) {
+      const unsigned u = key(i);
+      if (pass == 0 || (u >> (shift + bits)) == prefix) atomicAdd(&hist[(u >> shift) & ((1u << bits) - 1)], 1u);
+    }
+    __syncthreads();
+    {
+      const uint4 c = reinterpret_cast<const uint4 *>(hist)[t];
+      unsigned sum = (c.x + c.y) + (c.z + c.w);
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
+      if ((lane & 15) == 0) s_group[pass & 1][t >> 4] = sum;
     }
     cluster.sync();
-    // (The other buffer's counts were read before that barrier.)
-    for (int i = t; i < 256; i += kSelThr) {
-      unsigned x = 0;
-      for (int r = 0; r < ranks; ++r) x += cluster.map_shared_rank(hist, r)[i];
-      s_sum[i] = x;
-      s_hist[(pass + 1) & 1][i] = 0;
-    }
-    __syncthreads();
-    if (warp == 0) {  // lane l has the digits 255 - 8 l and the seven below
-      int c[8], sum = 0;
-#pragma unroll
-      for (int x = 0; x < 8; ++x) sum += c[x] = (int)s_sum[255 - 8 * lane - x];
-      int incl = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(~0u, incl, o);
-        if (lane >= o) incl += v;
+    // The other buffer's counts were read, by every CTA, before that barrier.
+    reinterpret_cast<uint4 *>(s_hist[(pass + 1) & 1])[t] = make_uint4(0, 0, 0, 0);
+    if (warp == 0) {
+      // The cluster's counts from the top: of the 32 groups, then of the 64 digits of the group where the sum
+      // reaches `want`, two to a lane.  (All of a cluster's counts would be 64 KB through distributed shared memory.)
+      int sum = 0;
+      for (int r = 0; r < ranks; ++r) sum += (int)cluster.map_shared_rank(s_group[pass & 1], r)[31 - lane];
+      int incl = warp_prefix(sum, lane);
+      const int at = __ffs(__ballot_sync(~0u, incl >= want)) - 1, group = 31 - at;
+      const int left = want - __shfl_sync(~0u, incl - sum, at);
+      const int digit = group * kGroup + kGroup - 1 - 2 * lane;
+      int c0 = 0, c1 = 0;
+      for (int r = 0; r < ranks; ++r) {
+        const unsigned *x = cluster.map_shared_rank(hist, r);
+        c0 += (int)x[digit];
+        c1 += (int)x[digit - 1];
       }
-      int left = want - (incl - sum);
-      if (left > 0 && left <= sum) {
-        int x = 0;
-#pragma unroll
-        for (; x < 7; ++x) {
-          if (left <= c[x]) break;
-          left -= c[x];
-        }
-        s_found[0] = 255 - 8 * lane - x;
-        s_found[1] = left;
+      incl = warp_prefix(c0 + c1, lane);
+      const int before = incl - c0 - c1;
+      if (before < left && left <= incl) {  // one lane
+        const bool second = left > before + c0;
+        s_found[0] = digit - (second ? 1 : 0);
+        s_found[1] = left - before - (second ? c0 : 0);
       }
     }
     __syncthreads();
-    prefix = (prefix << 8) | (unsigned)s_found[0];
+    prefix = (prefix << bits) | (unsigned)s_found[0];
     want = s_found[1];
   }
   const unsigned T = prefix;
@@ -165,14 +177,15 @@ __global__ void __launch_bounds__(kSelThr) cache_select_kernel(const __grid_cons
   }
   for (int i0 = a; i0 < z; i0 += 32) {
     const int i = i0 + lane;
-    const unsigned u = i < z ? key(i) : 0u;
+    const float wi = i < z ? weight(i) : 0.f;
+    const unsigned u = order_of(wi);
     const unsigned mg = __ballot_sync(~0u, i < z && u > T), me = __ballot_sync(~0u, i < z && u == T);
     const unsigned below = (1u << lane) - 1;
     const int e = e0 + __popc(me & below), g = g0 + __popc(mg & below);
     if (i < z && (u > T || (u == T && e < ties))) {
       const int at = p.first + g + min(e, ties);
       kept[at] = a0 + i;
-      w_out[at] = wp[i];
+      w_out[at] = wi;
     }
     g0 += __popc(mg);
     e0 += __popc(me);
@@ -180,90 +193,145 @@ __global__ void __launch_bounds__(kSelThr) cache_select_kernel(const __grid_cons
   cluster.sync();  // no CTA leaves while another reads its counts
 }
 
-// One block per (page of table_out, sequence, kv head, K or V): the rows that go there, read once and held
-// in registers (NP pieces of 16 codes per thread), their largest magnitude, their new scale, and their
-// new codes.  Bound by the gather of the rows; the chain position -> page -> scale is walked once per row,
-// into shared memory.
+// Four codes as two fp16 pairs, exactly, and back: codes * ratio rounded to the nearest code, for a
+// ratio that is a power of two in [2^-24, 2^15] (or 0) and results that do not exceed the largest code.
+template <int KIND> __device__ __forceinline__ void widen4(unsigned w, __half2 &lo, __half2 &hi) {
+  unsigned a, b;
+  if (KIND == ATTN_CACHE_E4M3) {
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}" : "=r"(a), "=r"(b) : "r"(w));
+    lo = *reinterpret_cast<__half2 *>(&a);
+    hi = *reinterpret_cast<__half2 *>(&b);
+  } else {  // code + 128 under the bits of 1024, less 1152
+    const unsigned u = w ^ 0x80808080u;
+    const __half2 bias = __half2half2(__ushort_as_half(0x6480));
+    a = __byte_perm(u, 0x64646464u, 0x4140);
+    b = __byte_perm(u, 0x64646464u, 0x4342);
+    lo = __hsub2(*reinterpret_cast<__half2 *>(&a), bias);
+    hi = __hsub2(*reinterpret_cast<__half2 *>(&b), bias);
+  }
+}
+template <int KIND> __device__ __forceinline__ unsigned narrow4(__half2 lo, __half2 hi, __half2 ratio) {
+  if (KIND == ATTN_CACHE_E4M3) {
+    // Exact products where it matters: below 2^-10 the code is 0, and four bits from there down are fp16's.
+    lo = __hmul2(lo, ratio);
+    hi = __hmul2(hi, ratio);
+    unsigned r;
+    asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e4m3x2.f16x2 x, %1;\n\tcvt.rn.satfinite.e4m3x2.f16x2 y, %2;\n\tmov.b32 %0, {x, y};\n\t}"
+        : "=r"(r) : "r"(*reinterpret_cast<unsigned *>(&lo)), "r"(*reinterpret_cast<unsigned *>(&hi)));
+    return r;
+  }
+  // One rounding, to an integer: 1.5 * 2^10 has a step of 1, and the low byte is the code.
+  const __half2 magic = __half2half2(__ushort_as_half(0x6600));
+  lo = __hfma2(lo, ratio, magic);
+  hi = __hfma2(hi, ratio, magic);
+  return __byte_perm(*reinterpret_cast<unsigned *>(&lo), *reinterpret_cast<unsigned *>(&hi), 0x6420);
+}
+
+// One block per (page of table_out, sequence, kv head): the K and V rows that go there, read once and held
+// in registers (NP pieces of 16 codes per thread, for each), their largest magnitudes, their new scales, and
+// their new codes.  The chain position -> page -> scales is walked once per row, into shared memory.  The
+// work per code is kept in fp16 pairs (exact) where the scales are powers of two, as this library's are: in
+// float it had taken longer than the memory.
 template <int KIND, int NP>
 __global__ void __launch_bounds__(kMoveThr) cache_move_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ float s_m[kMoveThr / 32], s_scale[128];
+  __shared__ float s_m[2][kMoveThr / 32], s_scale[2][128];
   __shared__ long long s_row[128];  // first code of each row, or -1
   grid_wait();
   const View &c = p.c;
   const int b = blockIdx.x / p.out_pages, nth = blockIdx.x - b * p.out_pages, h = blockIdx.y, t = threadIdx.x;
-  const bool val = blockIdx.z == 1;
-  const int n = min(seq_len(c, b), p.keep), i0 = nth << c.page_shift, rows = min(c.page, n - i0);
-  if (rows <= 0) return;
+  const int i0 = nth << c.page_shift;
   const int out = p.table_out[b * p.table_out_stride + nth];
+  const int pos = t < c.page && i0 + t < p.keep ? p.kept[((size_t)b * c.Hkv + h) * p.keep + i0 + t] : -1;
+  const int rows = min(c.page, min(seq_len(c, b), p.keep) - i0);
+  if (rows <= 0) return;
   if ((unsigned)out >= (unsigned)c.num_pages) {
     if (t == 0) set_status(c.status, kStatusBadPage);
     return;
   }
-  const uint8_t *codes = val ? c.v : c.k;
-  float *scales = val ? c.v_scale : c.k_scale;
   if (t < rows) {
-    const int pos = p.kept[((size_t)b * c.Hkv + h) * p.keep + i0 + t], page = page_of(c, b, pos);
+    const int page = page_of(c, b, pos);
+    const size_t at = (size_t)max(page, 0) * c.Hkv + h;
     s_row[t] = page < 0 ? -1 : (long long)row_at(c, page, h, pos & (c.page - 1));
-    s_scale[t] = page < 0 ? 0.f : scales[(size_t)page * c.Hkv + h];
+    s_scale[0][t] = page < 0 ? 0.f : c.k_scale[at];
+    s_scale[1][t] = page < 0 ? 0.f : c.v_scale[at];
   }
   __syncthreads();
   const int per = c.D / 16, total = rows * per;
-  uint4 w[NP];
-  float f[NP];
+  uint4 w[2][NP];
 #pragma unroll
   for (int x = 0; x < NP; ++x) {
     const int i = t + x * kMoveThr;
-    w[x] = make_uint4(0, 0, 0, 0);
-    f[x] = 0.f;
+    w[0][x] = w[1][x] = make_uint4(0, 0, 0, 0);
     if (i < total) {
       const int r = i / per, d = (i - r * per) * 16;
-      f[x] = s_scale[r];
-      if (s_row[r] >= 0) w[x] = *reinterpret_cast<const uint4 *>(codes + s_row[r] + d);
-    }
-  }
-  float amax = 0.f;
-#pragma unroll
-  for (int x = 0; x < NP; ++x) {
-    const unsigned u[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
-#pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      float v[4];
-      decode4<KIND>(u[y], v);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float m = fabsf(v[e] * f[x]);
-        if (m <= 3.402823466e38f) amax = fmaxf(amax, m);
+      if (s_row[r] >= 0) {
+        w[0][x] = *reinterpret_cast<const uint4 *>(c.k + s_row[r] + d);
+        w[1][x] = *reinterpret_cast<const uint4 *>(c.v + s_row[r] + d);
       }
     }
   }
+  float amax[2] = {0.f, 0.f};
 #pragma unroll
-  for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-  if ((t & 31) == 0) s_m[t >> 5] = amax;
+  for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+    for (int x = 0; x < NP; ++x) {
+      const int i = t + x * kMoveThr;
+      if (i >= total) continue;
+      const unsigned u[4] = {w[kv][x].x, w[kv][x].y, w[kv][x].z, w[kv][x].w};
+      __half2 m = __half2half2(__ushort_as_half(0));
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        __half2 lo, hi;
+        widen4<KIND>(u[y], lo, hi);
+        m = __hmax2(m, __hmax2(__habs2(lo), __habs2(hi)));  // (takes the other one where one is NaN)
+      }
+      amax[kv] = fmaxf(amax[kv], fmaxf(__low2float(m), __high2float(m)) * s_scale[kv][i / per]);
+    }
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) amax[kv] = fmaxf(amax[kv], __shfl_xor_sync(~0u, amax[kv], o));
+    if ((t & 31) == 0) s_m[kv][t >> 5] = amax[kv];
+  }
   __syncthreads();
 #pragma unroll
-  for (int x = 0; x < kMoveThr / 32; ++x) amax = fmaxf(amax, s_m[x]);
-  const float s = need_scale<KIND>(amax), inv = pow2_inverse(s);
-  uint4 *dst = reinterpret_cast<uint4 *>((val ? c.v : c.k) + row_at(c, out, h, 0));
+  for (int kv = 0; kv < 2; ++kv) {
 #pragma unroll
-  for (int x = 0; x < NP; ++x) {
-    const int i = t + x * kMoveThr;
-    if (i >= total) continue;
-    unsigned u[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+    for (int x = 0; x < kMoveThr / 32; ++x) amax[kv] = fmaxf(amax[kv], s_m[kv][x]);
+    const float s = need_scale<KIND>(fminf(amax[kv], 3.402823466e38f)), inv = pow2_inverse(s);
+    uint4 *dst = reinterpret_cast<uint4 *>((kv ? c.v : c.k) + row_at(c, out, h, 0));
 #pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      float v[4];
-      decode4<KIND>(u[y], v);
+    for (int x = 0; x < NP; ++x) {
+      const int i = t + x * kMoveThr;
+      if (i >= total) continue;
+      const float f = s_scale[kv][i / per], ratio = f * inv;
+      unsigned u[4] = {w[kv][x].x, w[kv][x].y, w[kv][x].z, w[kv][x].w};
+      if ((__float_as_uint(ratio) & 0x7fffffu) == 0u && ratio <= 32768.f) {
+        const __half2 r2 = __float2half2_rn(ratio);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = v[e] * f[x] * inv;  // the value (rounded to float), then an exact division
-      u[y] = encode2<KIND>(v[0], v[1]) | (encode2<KIND>(v[2], v[3]) << 16);
+        for (int y = 0; y < 4; ++y) {
+          __half2 lo, hi;
+          widen4<KIND>(u[y], lo, hi);
+          u[y] = narrow4<KIND>(lo, hi, r2);
+        }
+      } else {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          float v[4];
+          decode4<KIND>(u[y], v);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = v[e] * f * inv;  // the value (rounded to float), then an exact division
+          u[y] = encode2<KIND>(v[0], v[1]) | (encode2<KIND>(v[2], v[3]) << 16);
+        }
+      }
+      dst[i] = make_uint4(u[0], u[1], u[2], u[3]);
     }
-    dst[i] = make_uint4(u[0], u[1], u[2], u[3]);
+    if (t == 0) (kv ? c.v_scale : c.k_scale)[(size_t)out * c.Hkv + h] = s;
   }
-  if (t == 0) scales[(size_t)out * c.Hkv + h] = s;
 }
 
 template <int KIND> cudaError_t launch_move(const EvictParams &p, cudaStream_t st) {
-  const dim3 grid((unsigned)(p.c.B * p.out_pages), (unsigned)p.c.Hkv, 2);
+  const dim3 grid((unsigned)(p.c.B * p.out_pages), (unsigned)p.c.Hkv);
   const int pieces = (p.c.page * (p.c.D / 16) + kMoveThr - 1) / kMoveThr;  // at most 16: pages of 128 by 512
   if (pieces <= 1) return launch_dependent(cache_move_kernel<KIND, 1>, grid, kMoveThr, 0, st, p);
   if (pieces <= 2) return launch_dependent(cache_move_kernel<KIND, 2>, grid, kMoveThr, 0, st, p);
