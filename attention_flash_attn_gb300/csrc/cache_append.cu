@@ -149,16 +149,27 @@ __global__ void __launch_bounds__(kThr) cache_append_kernel(const __grid_constan
   const int D = c.D, per = D / 8, total = (last - first) * per, old = first & (c.page - 1);
   const long long ss = val ? p.v_ss : p.k_ss;
   const T *src = static_cast<const T *>(val ? p.v : p.k) + b * (val ? p.v_sb : p.k_sb) + h * (val ? p.v_sh : p.k_sh) + (first - len) * ss;
-  auto at = [&](int i) {
-    const int r = i / per;
-    return src + r * ss + (i - r * per) * 8;
+  // This thread's pieces: t, t + kThr, ... of the rows' pieces in order.
+  const int row0 = t / per, dr = kThr / per, dp = kThr - dr * per;
+  int piece = t - row0 * per;
+  const T *at = src + row0 * ss + piece * 8;
+  auto advance = [&]() {
+    piece += dp;
+    at += dr * ss + dp * 8;
+    if (piece >= per) {
+      piece -= per;
+      at += ss - per * 8;
+    }
   };
   Raw<T> held[kHeld];
 #pragma unroll
   for (int x = 0; x < kHeld; ++x) {
     held[x].zero();
-    if (t + x * kThr < total) held[x].load(at(t + x * kThr));
+    if (t + x * kThr < total) held[x].load(at);
+    advance();
   }
+  const T *const rest = at;
+  const int rest_piece = piece;
   const int page = page_of(c, b, first);
   if (!val && p.weights)
     for (int x = first + t; x < last; x += kThr) p.weights[b * p.w_sb + h * p.w_sh + x] = 0.f;
@@ -172,7 +183,8 @@ __global__ void __launch_bounds__(kThr) cache_append_kernel(const __grid_constan
 #pragma unroll 1
   for (int i = t + kHeld * kThr; i < total; i += kThr) {  // pages of more than 8192 values
     Raw<T> v;
-    v.load(at(i));
+    v.load(at);
+    advance();
     amax = max_nan(amax, v.amax());
   }
   amax = block_max(amax);  // (and every thread has read the old scale)
@@ -180,10 +192,13 @@ __global__ void __launch_bounds__(kThr) cache_append_kernel(const __grid_constan
   if (!fit) {  // something is infinite or NaN: the scale goes by the rest
     if (t == 0) set_status(c.status, kStatusNonFinite);
     amax = 0.f;
+    at = src + row0 * ss + (t - row0 * per) * 8;
+    piece = t - row0 * per;
 #pragma unroll 1
     for (int i = t; i < total; i += kThr) {
       Raw<T> v;
-      v.load(at(i));
+      v.load(at);
+      advance();
       float x[8];
       v.get(x);
       amax = amax_finite(x, amax);
@@ -202,10 +217,13 @@ __global__ void __launch_bounds__(kThr) cache_append_kernel(const __grid_constan
 #pragma unroll
   for (int x = 0; x < kHeld; ++x)
     if (t + x * kThr < total) put(t + x * kThr, held[x]);
+  at = rest;
+  piece = rest_piece;
 #pragma unroll 1
   for (int i = t + kHeld * kThr; i < total; i += kThr) {
     Raw<T> v;
-    v.load(at(i));
+    v.load(at);
+    advance();
     put(i, v);
   }
   if (old > 0 && s != was) rescale<KIND>(reinterpret_cast<uint4 *>(dst), old * (D / 16), was * inv, t, kThr);

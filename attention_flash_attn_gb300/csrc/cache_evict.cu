@@ -82,8 +82,15 @@ __global__ void __launch_bounds__(kSelThr) cache_select_kernel(const __grid_cons
   const int a0 = min(hi, lo + rank * part), cnt = min(hi, a0 + part) - a0;
   const float *wp = w + a0;
   if (in_smem) {
-#pragma unroll 16
-    for (int i = t; i < cnt; i += kSelThr) s_w[i] = wp[i];
+    // (Sixteen loads ahead of their stores: the compiler would not move them across.)
+    for (int i0 = t; i0 < cnt; i0 += 16 * kSelThr) {
+      float v[16];
+#pragma unroll
+      for (int x = 0; x < 16; ++x) v[x] = i0 + x * kSelThr < cnt ? wp[i0 + x * kSelThr] : 0.f;
+#pragma unroll
+      for (int x = 0; x < 16; ++x)
+        if (i0 + x * kSelThr < cnt) s_w[i0 + x * kSelThr] = v[x];
+    }
   }
   for (int i = t; i < kBins; i += kSelThr) s_hist[0][i] = 0;
   __syncthreads();
@@ -140,13 +147,33 @@ __global__ void __launch_bounds__(kSelThr) cache_select_kernel(const __grid_cons
   }
   const unsigned T = prefix;
   const int ties = want;  // positions equal to T that stay
-  const int wpart = ((cnt + kSelWarps - 1) / kSelWarps + 31) & ~31;
+  const int wpart = ((cnt + kSelWarps - 1) / kSelWarps + 127) & ~127;
   const int a = min(cnt, warp * wpart), z = min(cnt, a + wpart);
+  // Four neighbouring positions per lane; those past the end count as nothing.
+  auto four = [&](int i, float *v, unsigned *g, unsigned *e) {
+    *g = *e = 0;
+    if (in_smem && i + 4 <= z) {
+      const float4 q = *reinterpret_cast<const float4 *>(s_w + i);
+      v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    } else {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) v[x] = i + x < z ? weight(i + x) : 0.f;
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const unsigned u = order_of(v[x]);
+      *g |= (u > T && i + x < z ? 1u : 0u) << x;
+      *e |= (u == T && i + x < z ? 1u : 0u) << x;
+    }
+  };
   int gt = 0, eq = 0;
-  for (int i = a + lane; i < z; i += 32) {
-    const unsigned u = key(i);
-    gt += u > T;
-    eq += u == T;
+#pragma unroll 1
+  for (int i = a + 4 * lane; i < z; i += 128) {
+    float v[4];
+    unsigned g, e;
+    four(i, v, &g, &e);
+    gt += __popc(g);
+    eq += __popc(e);
   }
   gt = __reduce_add_sync(~0u, gt);
   eq = __reduce_add_sync(~0u, eq);
@@ -175,20 +202,30 @@ __global__ void __launch_bounds__(kSelThr) cache_select_kernel(const __grid_cons
     g0 += x[0];
     e0 += x[1];
   }
-  for (int i0 = a; i0 < z; i0 += 32) {
-    const int i = i0 + lane;
-    const float wi = i < z ? weight(i) : 0.f;
-    const unsigned u = order_of(wi);
-    const unsigned mg = __ballot_sync(~0u, i < z && u > T), me = __ballot_sync(~0u, i < z && u == T);
-    const unsigned below = (1u << lane) - 1;
-    const int e = e0 + __popc(me & below), g = g0 + __popc(mg & below);
-    if (i < z && (u > T || (u == T && e < ties))) {
-      const int at = p.first + g + min(e, ties);
-      kept[at] = a0 + i;
-      w_out[at] = wi;
+#pragma unroll 1
+  for (int i0 = a; i0 < z; i0 += 128) {
+    const int i = i0 + 4 * lane;
+    float v[4];
+    unsigned gm, em;
+    four(i, v, &gm, &em);
+    if (!__any_sync(~0u, gm | em)) continue;
+    // Both counts of the lanes before, in one prefix sum (at most 128 each).
+    const int both = __popc(gm) | (__popc(em) << 16), incl = warp_prefix(both, lane);
+    int g = g0 + ((incl - both) & 0xffff), e = e0 + ((incl - both) >> 16);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const bool is_g = (gm >> x) & 1u, is_e = (em >> x) & 1u;
+      if (is_g || (is_e && e < ties)) {
+        const int at = p.first + g + min(e, ties);
+        kept[at] = a0 + i + x;
+        w_out[at] = v[x];
+      }
+      g += is_g;
+      e += is_e;
     }
-    g0 += __popc(mg);
-    e0 += __popc(me);
+    const int all = __shfl_sync(~0u, incl, 31);
+    g0 += all & 0xffff;
+    e0 += all >> 16;
   }
   cluster.sync();  // no CTA leaves while another reads its counts
 }
@@ -258,15 +295,18 @@ __global__ void __launch_bounds__(kMoveThr) cache_move_kernel(const __grid_const
   __syncthreads();
   const int per = c.D / 16, total = rows * per;
   uint4 w[2][NP];
+  int row[NP];
 #pragma unroll
   for (int x = 0; x < NP; ++x) {
     const int i = t + x * kMoveThr;
     w[0][x] = w[1][x] = make_uint4(0, 0, 0, 0);
+    row[x] = i / per;
     if (i < total) {
-      const int r = i / per, d = (i - r * per) * 16;
-      if (s_row[r] >= 0) {
-        w[0][x] = *reinterpret_cast<const uint4 *>(c.k + s_row[r] + d);
-        w[1][x] = *reinterpret_cast<const uint4 *>(c.v + s_row[r] + d);
+      const long long at = s_row[row[x]];
+      if (at >= 0) {
+        const int d = (i - row[x] * per) * 16;
+        w[0][x] = *reinterpret_cast<const uint4 *>(c.k + at + d);
+        w[1][x] = *reinterpret_cast<const uint4 *>(c.v + at + d);
       }
     }
   }
@@ -275,8 +315,7 @@ __global__ void __launch_bounds__(kMoveThr) cache_move_kernel(const __grid_const
   for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
     for (int x = 0; x < NP; ++x) {
-      const int i = t + x * kMoveThr;
-      if (i >= total) continue;
+      if (t + x * kMoveThr >= total) continue;
       const unsigned u[4] = {w[kv][x].x, w[kv][x].y, w[kv][x].z, w[kv][x].w};
       __half2 m = __half2half2(__ushort_as_half(0));
 #pragma unroll
@@ -285,7 +324,7 @@ __global__ void __launch_bounds__(kMoveThr) cache_move_kernel(const __grid_const
         widen4<KIND>(u[y], lo, hi);
         m = __hmax2(m, __hmax2(__habs2(lo), __habs2(hi)));  // (takes the other one where one is NaN)
       }
-      amax[kv] = fmaxf(amax[kv], fmaxf(__low2float(m), __high2float(m)) * s_scale[kv][i / per]);
+      amax[kv] = fmaxf(amax[kv], fmaxf(__low2float(m), __high2float(m)) * s_scale[kv][row[x]]);
     }
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
@@ -304,7 +343,7 @@ __global__ void __launch_bounds__(kMoveThr) cache_move_kernel(const __grid_const
     for (int x = 0; x < NP; ++x) {
       const int i = t + x * kMoveThr;
       if (i >= total) continue;
-      const float f = s_scale[kv][i / per], ratio = f * inv;
+      const float f = s_scale[kv][row[x]], ratio = f * inv;
       unsigned u[4] = {w[kv][x].x, w[kv][x].y, w[kv][x].z, w[kv][x].w};
       if ((__float_as_uint(ratio) & 0x7fffffu) == 0u && ratio <= 32768.f) {
         const __half2 r2 = __float2half2_rn(ratio);
