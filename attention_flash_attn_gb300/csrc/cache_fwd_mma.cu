@@ -43,6 +43,7 @@ struct Cfg {
   static constexpr int CTAS = MT == 1 && D <= 128 ? 3 : 2;
   static constexpr bool QREG = D * MT <= 64;           // Q fragments in registers, else in shared memory
   static constexpr int ROWS = 16 * MT;
+  static_assert(NB == 1 || NH == 1, "a slice of several pages has one box per page");
   static constexpr size_t RING = (size_t)kWarps * DEPTH * STAGE;
   static_assert(DEPTH * STAGE >= ROWS * D * 4, "a warp's output fits its ring at the end of a run");
   static constexpr size_t Q_BYTES = QREG ? 0 : (size_t)MT * KS * 32 * 16;
@@ -59,22 +60,14 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, 
 }
 
 __device__ __forceinline__ void mma_f16(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t at) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
-  return v;
-}
+__device__ __forceinline__ uint4 lds128(const uint8_t *at) { return *reinterpret_cast<const uint4 *>(at); }
+__device__ __forceinline__ uint2 lds64(const uint8_t *at) { return *reinterpret_cast<const uint2 *>(at); }
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -120,7 +113,7 @@ template <int BLK> __device__ __forceinline__ uint32_t swz(int row, int ch) {
 // after the outputs that they belong to -- of the rows that see their key -- are marked in s_nan.  Only a
 // run's first and last slices come here, so it is kept small rather than fast: a key per lane.
 template <int KIND, int D, int MT>
-__device__ __noinline__ void scrub_values(const FwdParams &p, uint32_t sv, int pos, int key1, unsigned gone, int len, int r0, int rows,
+__device__ __noinline__ void scrub_values(const FwdParams &p, uint8_t *sv, int pos, int key1, unsigned gone, int len, int r0, int rows,
                                           uint32_t *s_nan, int *s_any) {
   using C = Cfg<D, MT>;
   const int lane = threadIdx.x & 31;
@@ -129,7 +122,7 @@ __device__ __noinline__ void scrub_values(const FwdParams &p, uint32_t sv, int p
     const bool hide = pos + row >= key1 || ((gone >> (row >> 4)) & 1u);
 #pragma unroll 1
     for (int c = 0; c < D / 16; ++c) {
-      const uint32_t at = sv + (c * 16 / C::BLK) * (C::SK * C::BLK) + swz<C::BLK>(row, c % (C::BLK / 16));
+      uint8_t *at = sv + (c * 16 / C::BLK) * (C::SK * C::BLK) + swz<C::BLK>(row, c % (C::BLK / 16));
       uint4 u = lds128(at);
       uint32_t w[4] = {u.x, u.y, u.z, u.w};
       bool write = hide;
@@ -155,7 +148,7 @@ __device__ __noinline__ void scrub_values(const FwdParams &p, uint32_t sv, int p
           }
         }
       }
-      if (write) asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+      if (write) *reinterpret_cast<uint4 *>(at) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the stage's next fill comes by TMA
@@ -198,6 +191,8 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
   int stage = 0;
   bool dead = false;    // a wait gave up: recorded; this warp computes no further
   const float cap_log2 = p.cap * kLog2e;
+  int id_nxt[C::NH];
+  bool first = true;    // (id_nxt holds the page ids of every run but the first)
 #pragma unroll 1
   while (cursor_next(p, cur, run)) {
     const int r0 = run.rt * C::ROWS, rows = min(C::ROWS, p.R - r0);
@@ -206,70 +201,99 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
     const int n_slices = (key1 - key0 - warp * C::SK + kWarps * C::SK - 1) / (kWarps * C::SK);  // <= 0: none
 
     // Page ids and scales of 32 slices, one per lane, and the following batch's page ids.
-    int id_now[C::NH], id_nxt[C::NH];
+    int id_now[C::NH];
     float ks_now[C::NH], lv_now[C::NH];
     unsigned odd_now = 0;  // bit x: slice x of the batch has a half without a page, or whose values count as 0
-    auto load_ids = [&](int batch, int *ids) {
-      const int x = batch * 32 + lane;
+    auto load_ids = [&](int b, int from, int to, int batch, int *ids) {  // of the warp's slices in [from, to)
 #pragma unroll
       for (int h = 0; h < C::NH; ++h) {
-        const int pos = key0 + (warp + kWarps * x) * C::SK + 16 * h;
-        ids[h] = x < n_slices && pos < key1 ? page_of(p.c, run.b, pos) : -1;
+        const int pos = from + (warp + kWarps * (batch * 32 + lane)) * C::SK + 16 * h;
+        ids[h] = pos < to ? page_of(p.c, b, pos) : -1;
       }
     };
-    // A value scale that counts as 0 has kZeroLog for its logarithm: any reference does for values of 0, as
-    // long as the sum undoes it.
-    auto load_scales = [&]() {
-      bool odd = false;
+    // The page ids that follow batch `batch`: of this run's next one, or of the next run's first.
+    auto load_next_ids = [&](int batch) {
+      if (n_slices > batch * 32 + 32) {
+        load_ids(run.b, key0, key1, batch + 1, id_nxt);
+      } else {
+        Cursor peek = cur;
+        Run next;
+        if (cursor_next(p, peek, next)) {
+          const int from = next.range.lo + (next.off << p.unit_shift);
+          load_ids(next.b, from, min(next.range.hi, from + (next.cnt << p.unit_shift)), 0, id_nxt);
+        }
+      }
+    };
+    // The scales of the batch in id_now, in two steps, so that nothing waits for them before the first
+    // slice has come.  A value scale that counts as 0 has kZeroLog for its logarithm: any reference does for
+    // values of 0, as long as the sum undoes it.
+    auto fetch_scales = [&]() {
 #pragma unroll
       for (int h = 0; h < C::NH; ++h) {
-        ks_now[h] = 0.f;
-        float vs = 0.f;
+        ks_now[h] = lv_now[h] = 0.f;
         if (id_now[h] >= 0) {
           const size_t at = (size_t)id_now[h] * p.c.Hkv + run.hk;
           ks_now[h] = p.c.k_scale[at];
-          vs = p.c.v_scale[at];
+          lv_now[h] = p.c.v_scale[at];
         }
-        lv_now[h] = vs >= kMinScale ? log2f(vs) : kZeroLog;
-        odd |= !(vs >= kMinScale);
+      }
+    };
+    auto take_scales = [&]() {
+      bool odd = false;
+#pragma unroll
+      for (int h = 0; h < C::NH; ++h) {
+        odd |= !(lv_now[h] >= kMinScale);
+        lv_now[h] = lv_now[h] >= kMinScale ? log2f(lv_now[h]) : kZeroLog;
       }
       odd_now = __ballot_sync(~0u, odd);
     };
-    // Fills ring stage `st` with slice x (ids: its batch).  All lanes call it; lane 0 issues.
+    // Fills ring stage `st` with slice x (ids: its batch).  All lanes call it; lane 0 issues, or, where a
+    // slice spans several pages, a lane for each.
     auto issue = [&](int x, int st, const int *ids) {
       const uint32_t bar = bars + 8 * st, dst = ring + st * C::STAGE;
-      int id[C::NH];
+      const int pos = key0 + (warp + kWarps * x) * C::SK;
+      const int slot = pos & (p.c.page - 1);
+      int id = __shfl_sync(~0u, ids[0], x & 31);
+      if (C::NH == 1 || p.c.page >= C::SK) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, id >= 0 ? C::STAGE : 0);
+          if (id >= 0) {
+            const int head = id * p.c.Hkv + run.hk;
 #pragma unroll
-      for (int h = 0; h < C::NH; ++h) id[h] = __shfl_sync(~0u, ids[h], x & 31);
-      if (lane == 0) {
-        const int pos = key0 + (warp + kWarps * x) * C::SK;
-        const int box = min(p.c.page, C::SK);  // rows of one load
-        uint32_t bytes = 0;
-#pragma unroll
-        for (int h = 0; h < C::NH; ++h)
-          if (16 * h % box == 0 && id[h] >= 0) bytes += 2 * D * box;
-        mbar_arrive_expect_tx(bar, bytes);
-#pragma unroll
-        for (int h = 0; h < C::NH; ++h) {
-          if (16 * h % box != 0 || id[h] < 0) continue;
-          const int head = id[h] * p.c.Hkv + run.hk;
-#pragma unroll
-          for (int j = 0; j < C::NB; ++j) {
-            const uint32_t to = dst + j * (C::SK * C::BLK) + h * (16 * C::BLK);
-            tma_load_3d(to, &kmap, bar, j * C::BLK, (pos + 16 * h) & (p.c.page - 1), head);
-            tma_load_3d(to + C::SK * D, &vmap, bar, j * C::BLK, (pos + 16 * h) & (p.c.page - 1), head);
+            for (int j = 0; j < C::NB; ++j) {
+              tma_load_3d(dst + j * (C::SK * C::BLK), &kmap, bar, j * C::BLK, slot, head);
+              tma_load_3d(dst + C::SK * D + j * (C::SK * C::BLK), &vmap, bar, j * C::BLK, slot, head);
+            }
           }
+        }
+      } else {
+        const int boxes = C::SK >> p.c.page_shift, groups = C::NH / boxes;  // (each slice begins a page)
+#pragma unroll
+        for (int h = 1; h < C::NH; ++h) {
+          const int other = __shfl_sync(~0u, ids[h], x & 31);
+          if (h == lane * groups) id = other;
+        }
+        const bool has = lane < boxes && id >= 0;
+        const unsigned count = __popc(__ballot_sync(~0u, has));
+        if (lane == 0) mbar_arrive_expect_tx(bar, count * (2 * D << p.c.page_shift));
+        __syncwarp();
+        if (has) {
+          const int head = id * p.c.Hkv + run.hk;
+          const uint32_t to = dst + ((lane * C::BLK) << p.c.page_shift);
+          tma_load_3d(to, &kmap, bar, 0, 0, head);
+          tma_load_3d(to + C::SK * D, &vmap, bar, 0, 0, head);
         }
       }
     };
 
-    load_ids(0, id_now);
+    if (first) load_ids(run.b, key0, key1, 0, id_nxt);
+    first = false;
+#pragma unroll
+    for (int h = 0; h < C::NH; ++h) id_now[h] = id_nxt[h];
 #pragma unroll 1
     for (int s = 0; s < min(C::DEPTH, n_slices); ++s) issue(s, stage + s >= C::DEPTH ? stage + s - C::DEPTH : stage + s, id_now);
-    load_scales();
-#pragma unroll
-    for (int h = 0; h < C::NH; ++h) id_nxt[h] = -1;
-    if (n_slices > 32) load_ids(1, id_nxt);
+    fetch_scales();
+    load_next_ids(0);
 
     // Queries: rows g and g + 8 of each 16, this lane's columns, scaled into fp16.
     uint32_t qf[C::QREG ? MT : 1][C::QREG ? C::KS : 1][4];
@@ -359,9 +383,13 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
       if (x > 0 && (x & 31) == 0) {
 #pragma unroll
         for (int h = 0; h < C::NH; ++h) id_now[h] = id_nxt[h];
-        load_scales();
-        if (n_slices > (x | 31) + 1) load_ids((x >> 5) + 1, id_nxt);
+        fetch_scales();
+        load_next_ids(x >> 5);
       }
+      uint8_t *const sk = base + (warp * C::DEPTH + stage) * C::STAGE, *const sv = sk + C::SK * D;
+      if (!dead) dead = !__all_sync(~0u, mbar_wait(bars + 8 * stage, (phases >> stage) & 1u, p.c.status));
+      phases ^= 1u << stage;
+      if ((x & 31) == 0) take_scales();
       // This slice's scales.
       float ks[C::NH], lv[C::NH];
 #pragma unroll
@@ -370,9 +398,6 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
         lv[h] = __shfl_sync(~0u, lv_now[h], x & 31);
       }
       const bool partial = ((odd_now >> (x & 31)) & 1u) || pos + C::SK > all_below || pos < all_from;
-      const uint32_t sk = ring + stage * C::STAGE, sv = sk + C::SK * D;
-      if (!dead) dead = !__all_sync(~0u, mbar_wait(bars + 8 * stage, (phases >> stage) & 1u, p.c.status));
-      phases ^= 1u << stage;
       if (!dead) {
         float s[MT][C::SK / 8][4];
 #pragma unroll
@@ -540,7 +565,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               // Key 16 h + 8 (q >> 1) + 2 t + (q & 1): its low three bits, which the swizzle uses, are the last two terms.
-              const uint32_t at = sv + j * (C::SK * C::BLK) + (16 * h + 8 * (q >> 1)) * C::BLK;
+              const uint8_t *at = sv + j * (C::SK * C::BLK) + (16 * h + 8 * (q >> 1)) * C::BLK;
               if (C::BLK == 128) {
                 const uint4 u = lds128(at + swz<C::BLK>(2 * t + (q & 1), g));
                 vw[q][0] = u.x;
