@@ -56,10 +56,11 @@ __global__ void __launch_bounds__(kThreads) cache_fwd_simt_kernel(const __grid_c
   float *my_p = s_p + warp * kRows * 32;
 
   grid_launch_next();  // (one wave of CTAs: the join's blocks take nobody's place)
+  __shared__ Groups s_groups;
   Cursor cur;
-  if (!cursor_begin(p, cur)) return;
+  if (!cursor_begin(p, &s_groups, cur)) return;
   Run run;
-  while (cursor_next(p, cur, run)) {
+  while (cursor_next(p, &s_groups, cur, run)) {
     const int r0 = run.rt * kRows, rows = min(kRows, p.R - r0);
     __syncthreads();  // the previous run has left shared memory
     for (int x = t; x < kRows * D / 4; x += kThreads) {
@@ -263,43 +264,67 @@ __global__ void __launch_bounds__(kThreads) cache_join_kernel(const __grid_const
   const int second = n > 0 && s > sh.begin(c0) ? 1 : 0;
   auto part = [&](int c) { return (size_t)(2 * c + (c == c0 ? second : 0)) * p.row_tile + sub; };
   const int me = PER_ROW > 1 ? warp : 0;
-  float M = -CUDART_INF_F;
-  for (int c = c0 + me * 32 + lane; c <= c1; c += PER_ROW * 32) M = max_nan(M, p.ml_part[part(c)].x);
-  M = warp_max(M);
-  if (PER_ROW > 1) {
-    if (lane == 0) s_ml[warp].x = M;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < PER_ROW; ++w) M = max_nan(M, s_ml[w].x);
-  }
-  float L = 0.f;
+  // Running maximum and sum over this warp's parts, four at a time, loads first.
+  float M = -CUDART_INF_F, L = 0.f;
   float4 acc[4];  // 512 columns
 #pragma unroll
   for (int x = 0; x < 4; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int c = c0 + me; c <= c1; c += PER_ROW) {
-    const size_t at = part(c);
-    const float2 ml = p.ml_part[at];
-    if (ml.x == -CUDART_INF_F) continue;
-    const float f = exp2f(ml.x - M);
-    L += ml.y * f;
+#pragma unroll 1
+  for (int c = c0 + me; c <= c1; c += 4 * PER_ROW) {
+    float2 ml[4];
+    size_t at[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int ci = c + i * PER_ROW;
+      at[i] = part(min(ci, c1));
+      ml[i] = ci <= c1 ? p.ml_part[at[i]] : make_float2(-CUDART_INF_F, 0.f);
+    }
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       const int d = x * 128 + lane * 4;
-      if (d < D) {
-        const float4 v = *reinterpret_cast<const float4 *>(p.o_part + at * D + d);
-        acc[x].x += f * v.x; acc[x].y += f * v.y; acc[x].z += f * v.z; acc[x].w += f * v.w;
+      if (x * 128 >= D) break;
+      float4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = d < D ? *reinterpret_cast<const float4 *>(p.o_part + at[i] * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+      float top = M;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = max_nan(top, ml[i].x);
+      const float a = top == -CUDART_INF_F ? 1.f : exp2f(M - top);
+      acc[x].x *= a; acc[x].y *= a; acc[x].z *= a; acc[x].w *= a;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (ml[i].x == -CUDART_INF_F) continue;
+        const float f = exp2f(ml[i].x - top);
+        acc[x].x += f * v[i].x; acc[x].y += f * v[i].y; acc[x].z += f * v[i].z; acc[x].w += f * v[i].w;
       }
     }
-  }
-  if (PER_ROW > 1) {
-    if (lane == 0) s_ml[warp].y = L;
+    float top = M;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) s_o[warp][PER_ROW > 1 ? x * 32 + lane : 0] = acc[x];
+    for (int i = 0; i < 4; ++i) top = max_nan(top, ml[i].x);
+    L *= top == -CUDART_INF_F ? 1.f : exp2f(M - top);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (ml[i].x != -CUDART_INF_F) L += ml[i].y * exp2f(ml[i].x - top);
+    M = top;
+  }
+  if (PER_ROW > 1) {  // the warps' parts of the row
+    if (lane == 0) s_ml[warp] = make_float2(M, L);
     __syncthreads();
+    const float mine = M;
     L = 0.f;
 #pragma unroll
-    for (int w = 0; w < PER_ROW; ++w) L += s_ml[w].y;
+    for (int w = 0; w < PER_ROW; ++w) M = max_nan(M, s_ml[w].x);
+#pragma unroll
+    for (int w = 0; w < PER_ROW; ++w)
+      if (s_ml[w].x != -CUDART_INF_F) L += s_ml[w].y * exp2f(s_ml[w].x - M);
+    const float f = mine == -CUDART_INF_F ? 0.f : exp2f(mine - M);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (x * 128 >= D) break;
+      s_o[warp][PER_ROW > 1 ? x * 32 + lane : 0] = make_float4(f * acc[x].x, f * acc[x].y, f * acc[x].z, f * acc[x].w);
+    }
+    __syncthreads();
   }
   const RowEnd e = row_end(p, hk * p.G + r % p.G, M, L);
   const bool none = M == -CUDART_INF_F;

@@ -38,6 +38,7 @@ struct Cfg {
   static constexpr int KS = D / 16;                    // k-steps of Q K^T
   static constexpr int NT = D / 8;                     // n-tiles of P V
   static constexpr int QG = SK < 32 ? SK / 8 : 4;      // n-tiles of Q K^T whose codes are in registers at once
+  static constexpr bool SPLIT = D == 256;               // scores in two accumulators
   static constexpr int STAGE = 2 * SK * D;             // bytes of a slice, K then V
   static constexpr int DEPTH = 2;
   static constexpr int CTAS = MT == 1 && D <= 128 ? 3 : 2;
@@ -181,8 +182,9 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
   if (tid == 0) s_any = 0;
   __syncwarp();
 
+  __shared__ Groups s_groups;
   Cursor cur;
-  if (!cursor_begin(p, cur)) {
+  if (!cursor_begin(p, &s_groups, cur)) {
     grid_launch_next();
     return;
   }
@@ -194,7 +196,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
   int id_nxt[C::NH];
   bool first = true;    // (id_nxt holds the page ids of every run but the first)
 #pragma unroll 1
-  while (cursor_next(p, cur, run)) {
+  while (cursor_next(p, &s_groups, cur, run)) {
     const int r0 = run.rt * C::ROWS, rows = min(C::ROWS, p.R - r0);
     const int key0 = run.range.lo + (run.off << p.unit_shift), key1 = min(run.range.hi, key0 + (run.cnt << p.unit_shift));
     // This warp's slices: key0 + (warp + 4 x) SK for x < n_slices.
@@ -218,7 +220,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
       } else {
         Cursor peek = cur;
         Run next;
-        if (cursor_next(p, peek, next)) {
+        if (cursor_next(p, &s_groups, peek, next)) {
           const int from = next.range.lo + (next.off << p.unit_shift);
           load_ids(next.b, from, min(next.range.hi, from + (next.cnt << p.unit_shift)), 0, id_nxt);
         }
@@ -286,6 +288,21 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
       }
     };
 
+    // Queries: rows g and g + 8 of each 16, this lane's columns; asked for before anything that waits.
+    uint4 raw_q[MT][2][D / 32];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int r = r0 + mt * 16 + 8 * y + g, i = query_of(p, r), h = run.hk * p.G + (r - i * p.G);
+        const __nv_bfloat16 *row = static_cast<const __nv_bfloat16 *>(p.q) + run.b * p.q_sb + i * p.q_ss + h * p.q_sh + t * (C::BLK / 4);
+#pragma unroll
+        for (int z = 0; z < D / 32; ++z) {
+          raw_q[mt][y][z] = make_uint4(0, 0, 0, 0);
+          if (r < p.R) raw_q[mt][y][z] = *reinterpret_cast<const uint4 *>(row + (z / (C::BLK / 32)) * C::BLK + (z % (C::BLK / 32)) * 8);
+        }
+      }
+
     if (first) load_ids(run.b, key0, key1, 0, id_nxt);
     first = false;
 #pragma unroll
@@ -295,32 +312,21 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
     fetch_scales();
     load_next_ids(0);
 
-    // Queries: rows g and g + 8 of each 16, this lane's columns, scaled into fp16.
+    // The queries scaled into fp16.
     uint32_t qf[C::QREG ? MT : 1][C::QREG ? C::KS : 1][4];
     float q_mul[MT][2];  // what undoes the scaling, times the softmax scale (and log2 e without a cap)
     int see_lo[MT][2], see_n[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      uint4 raw_q[2][D / 32];
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const int r = r0 + mt * 16 + 8 * y + g;
-        const int i = query_of(p, r), h = run.hk * p.G + (r - i * p.G);
-        const int2 see = row_sees(p, run.range.len, i);
+        const int2 see = row_sees(p, run.range.len, query_of(p, r0 + mt * 16 + 8 * y + g));
         see_lo[mt][y] = see.x;
         see_n[mt][y] = max(0, min(see.y, key1) - see.x);
         float amax = 0.f;
 #pragma unroll
         for (int z = 0; z < D / 32; ++z) {
-          raw_q[y][z] = make_uint4(0, 0, 0, 0);
-          if (r < p.R)
-            raw_q[y][z] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + run.b * p.q_sb + i * p.q_ss +
-                                                           h * p.q_sh + (z / (C::BLK / 32)) * C::BLK + t * (C::BLK / 4) +
-                                                           (z % (C::BLK / 32)) * 8);
-        }
-#pragma unroll
-        for (int z = 0; z < D / 32; ++z) {
-          const uint32_t w[4] = {raw_q[y][z].x, raw_q[y][z].y, raw_q[y][z].z, raw_q[y][z].w};
+          const uint32_t w[4] = {raw_q[mt][y][z].x, raw_q[mt][y][z].y, raw_q[mt][y][z].z, raw_q[mt][y][z].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             amax = max_nan(amax, max_nan(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
@@ -335,7 +341,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
         q_mul[mt][y] = __uint_as_float((unsigned)(127 - x) << 23) * fabsf(p.scale) * (p.cap > 0.f ? 2.f * kLog2e * p.inv_cap : kLog2e);
 #pragma unroll
         for (int z = 0; z < D / 32; ++z) {
-          uint4 &u = raw_q[y][z];
+          uint4 &u = raw_q[mt][y][z];
           uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -346,7 +352,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
       // A fragment of k-step s: columns 4 s .. 4 s + 3 of this lane's (words 2 s and 2 s + 1).
 #pragma unroll
       for (int s = 0; s < C::KS; ++s) {
-        const uint4 &u = raw_q[0][s / 2], &v = raw_q[1][s / 2];
+        const uint4 &u = raw_q[mt][0][s / 2], &v = raw_q[mt][1][s / 2];
         const uint4 f = s % 2 ? make_uint4(u.z, v.z, u.w, v.w) : make_uint4(u.x, v.x, u.y, v.y);
         if (C::QREG) {
           qf[C::QREG ? mt : 0][C::QREG ? s : 0][0] = f.x;
@@ -399,13 +405,14 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
       }
       const bool partial = ((odd_now >> (x & 31)) & 1u) || pos + C::SK > all_below || pos < all_from;
       if (!dead) {
-        float s[MT][C::SK / 8][4];
+        // (Two accumulators where few n-tiles would make the k-steps one long chain.)
+        float s[MT][C::SK / 8][4], s2[MT][C::SPLIT ? C::SK / 8 : 1][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int n = 0; n < C::SK / 8; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
+            for (int e = 0; e < 4; ++e) s[mt][n][e] = s2[mt][C::SPLIT ? n : 0][e] = 0.f;
         // Scores: n-tile n holds keys 8 n .. 8 n + 7, key 8 n + g on the lanes of group g.
 #pragma unroll
         for (int j = 0; j < C::NB; ++j)
@@ -435,12 +442,20 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
                       mma_f16(s[mt][n0 + n], qf[C::QREG ? mt : 0][C::QREG ? step : 0], b0, b1);
                     } else {
                       const uint32_t a[4] = {qs[mt].x, qs[mt].y, qs[mt].z, qs[mt].w};
-                      mma_f16(s[mt][n0 + n], a, b0, b1);
+                      mma_f16(C::SPLIT && (w & 1) ? s2[mt][C::SPLIT ? n0 + n : 0] : s[mt][n0 + n], a, b0, b1);
                     }
                   }
                 }
               }
             }
+        if (C::SPLIT) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int n = 0; n < C::SK / 8; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[mt][n][e] += s2[mt][C::SPLIT ? n : 0][e];
+        }
         // Softmax.  A probability is 2^(f s + lv - m): f takes a raw score to a logit in base 2 (it is not
         // negative, so that the largest raw score gives the largest logit), lv is the values' scale.  With a cap
         // or a mask the logits are formed first, and f is 1.

@@ -34,44 +34,67 @@ struct Run {
   Range range;
 };
 
-__device__ __forceinline__ int group_units(const FwdParams &p, int g) {
+__device__ __forceinline__ Range range_of(const FwdParams &p, int g) {
   const int b = p.RT == 1 ? g : g / p.RT;
-  return range_units(p, group_range(p, b, g - b * p.RT));
+  return group_range(p, b, g - b * p.RT);
 }
 
-// Called by all kThreads threads; false if this CTA has no units.  CTA 0 stores the prefix sums and
-// records lengths outside the table.  Each thread has a contiguous part of the groups.
-__device__ __forceinline__ bool cursor_begin(const FwdParams &p, Cursor &cur) {
+// The groups' ranges in shared memory, where they fit: few groups are the calls that take microseconds,
+// and each would be read from memory and worked out again for every run.
+struct Groups {
+  int4 r[32];  // lo, hi, len, units
+};
+__device__ __forceinline__ bool few_groups(const FwdParams &p) { return p.NG <= 32; }
+
+// False if this CTA has no units.  CTA 0 stores the prefix sums and records lengths outside the table.
+// Called by all kThreads threads.  Few groups: every warp does it all, a group per lane, with no
+// barrier; many: each thread has a contiguous part of them.
+__device__ __forceinline__ bool cursor_begin(const FwdParams &p, Groups *few, Cursor &cur) {
   __shared__ int s_sum[kThreads / 32], s_at[2];
-  const int t = threadIdx.x, per = (p.NG + kThreads - 1) / kThreads;
-  const int g0 = min(p.NG, t * per), g1 = min(p.NG, g0 + per);
-  int sum = 0;
+  const int t = threadIdx.x, lane = t & 31;
+  int Uh = 0, excl, sum = 0, g0, per = 1;
+  if (few_groups(p)) {
+    g0 = lane;
+    if (lane < p.NG) {
+      const Range r = range_of(p, lane);
+      sum = range_units(p, r);
+      few->r[lane] = make_int4(r.lo, r.hi, r.len, sum);  // (every warp writes the same)
+    }
+  } else {
+    per = (p.NG + kThreads - 1) / kThreads;
+    g0 = min(p.NG, t * per);
 #pragma unroll 1
-  for (int g = g0; g < g1; ++g) sum += group_units(p, g);
+    for (int g = g0; g < min(p.NG, g0 + per); ++g) sum += range_units(p, range_of(p, g));
+  }
   int incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(~0u, incl, o);
-    if ((t & 31) >= o) incl += v;
+    if (lane >= o) incl += v;
   }
-  if ((t & 31) == 31) s_sum[t >> 5] = incl;
-  __syncthreads();
-  int excl = incl - sum, Uh = 0;
+  excl = incl - sum;
+  if (few_groups(p)) {
+    Uh = __shfl_sync(~0u, incl, 31);
+    __syncwarp();
+  } else {
+    if (lane == 31) s_sum[t >> 5] = incl;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < (t >> 5)) excl += s_sum[w];
-    Uh += s_sum[w];
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < (t >> 5)) excl += s_sum[w];
+      Uh += s_sum[w];
+    }
   }
-  if (blockIdx.x == 0) {
+  if (blockIdx.x == 0 && (t < 32 || !few_groups(p))) {
     int x = excl;
 #pragma unroll 1
-    for (int g = g0; g < g1; ++g) {
+    for (int g = g0; g < min(p.NG, g0 + per); ++g) {
       p.prefix[g] = x;
-      x += group_units(p, g);
+      x += range_units(p, range_of(p, g));
     }
-    if (t == kThreads - 1) p.prefix[p.NG] = Uh;
+    if (t == 0) p.prefix[p.NG] = Uh;
 #pragma unroll 1
-    for (int b = t; b < p.c.B; b += kThreads) {
+    for (int b = t; b < p.c.B; b += few_groups(p) ? 32 : kThreads) {
       bool bad;
       seq_len(p.c, b, &bad);
       if (bad) set_status(p.c.status, kStatusBadPage);
@@ -84,11 +107,18 @@ __device__ __forceinline__ bool cursor_begin(const FwdParams &p, Cursor &cur) {
   cur.u1 = sh.begin(blockIdx.x + 1);
   cur.hk = cur.u / Uh;
   const int r = cur.u - cur.hk * Uh;
-  if (excl <= r && r < excl + sum) {
+  const bool here = excl <= r && r < excl + sum;
+  if (few_groups(p)) {
+    const int at = __ffs(__ballot_sync(~0u, here)) - 1;
+    cur.g = at;
+    cur.g_first = cur.hk * Uh + __shfl_sync(~0u, excl, at);
+    return true;
+  }
+  if (here) {
     int x = excl, g = g0;
 #pragma unroll 1
     for (;; ++g) {
-      const int n = group_units(p, g);
+      const int n = range_units(p, range_of(p, g));
       if (r < x + n) break;
       x += n;
     }
@@ -102,14 +132,20 @@ __device__ __forceinline__ bool cursor_begin(const FwdParams &p, Cursor &cur) {
 }
 
 // The next run of this CTA; false when there is none.  Uniform over the CTA.
-__device__ __forceinline__ bool cursor_next(const FwdParams &p, Cursor &cur, Run &run) {
+__device__ __forceinline__ bool cursor_next(const FwdParams &p, const Groups *few, Cursor &cur, Run &run) {
   if (cur.u >= cur.u1) return false;
 #pragma unroll 1
   for (;;) {
-    run.b = p.RT == 1 ? cur.g : cur.g / p.RT;
-    run.rt = cur.g - run.b * p.RT;
-    run.range = group_range(p, run.b, run.rt);
-    run.n = range_units(p, run.range);
+    if (few_groups(p)) {
+      const int4 r = few->r[cur.g];
+      run.range.lo = r.x;
+      run.range.hi = r.y;
+      run.range.len = r.z;
+      run.n = r.w;
+    } else {
+      run.range = range_of(p, cur.g);
+      run.n = range_units(p, run.range);
+    }
     if (cur.u < cur.g_first + run.n) break;
     cur.g_first += run.n;
     if (++cur.g == p.NG) {
@@ -117,6 +153,8 @@ __device__ __forceinline__ bool cursor_next(const FwdParams &p, Cursor &cur, Run
       ++cur.hk;
     }
   }
+  run.b = p.RT == 1 ? cur.g : cur.g / p.RT;
+  run.rt = cur.g - run.b * p.RT;
   run.hk = cur.hk;
   run.off = cur.u - cur.g_first;
   run.cnt = min(run.n - run.off, cur.u1 - cur.u);
