@@ -137,13 +137,17 @@ FwdParams fwd_params(const attn_cache *c, const attn_cache_seqs *s, const attn_c
   p.w_sb = a->weights_stride_b;
   p.w_sh = a->weights_stride_h;
   p.Lpad = (cap + 63) / 64 * 64;
+  if (mma) p.cluster = mma_cluster(p);
   size_t off = 0;
-  L->prefix = off; off += align_up(((size_t)p.NG + 1) * sizeof(int));
-  L->o_part = off; off += align_up((size_t)2 * p.max_ctas * p.row_tile * c->D * sizeof(float));
-  L->ml_part = off; off += align_up((size_t)2 * p.max_ctas * p.row_tile * sizeof(float2));
+  L->prefix = L->o_part = L->ml_part = 0;
+  if (!p.cluster) {
+    L->prefix = off; off += align_up(((size_t)p.NG + 1) * sizeof(int));
+    L->o_part = off; off += align_up((size_t)2 * p.max_ctas * p.row_tile * c->D * sizeof(float));
+    L->ml_part = off; off += align_up((size_t)2 * p.max_ctas * p.row_tile * sizeof(float2));
+  }
   L->scores = off;
   if (a->weights) off += align_up((size_t)s->B * c->Hkv * p.R * p.Lpad * sizeof(float));
-  L->total = off;
+  L->total = std::max(off, kAlign);
   return p;
 }
 
@@ -221,7 +225,7 @@ int attn_cache_fwd(const attn_cache *c, const attn_cache_seqs *s, const attn_cac
   p.LSE = LSE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = use_mma(c, a) ? launch_fwd_mma(p, c->kind, st) : launch_fwd_simt(p, a->dtype, c->kind, st);
-  if (e == cudaSuccess) e = launch_fwd_join(p, a->dtype, st);
+  if (e == cudaSuccess && !p.cluster) e = launch_fwd_join(p, a->dtype, st);
   if (e == cudaSuccess && a->weights && s->max_pages > 0) e = launch_weights(p, st);
   return cuda_status(e);
 }

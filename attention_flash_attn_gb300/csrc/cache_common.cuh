@@ -127,6 +127,7 @@ struct FwdParams {
   int Sq, Hq, G, R;      // R = G * Sq: query rows of one (sequence, kv head); row r is query r / G,
                          // head h * G + r % G
   int row_tile, NG, RT;  // rows per work item; RT = ceil(R / row_tile); NG = B * RT groups (b, tile)
+  int cluster;           // CTAs of the cluster that has an item (tensor-core path), or 0: items split over the grid
   int unit_shift;        // keys of one unit of work: a slice for each warp of a CTA
   int max_ctas;
   int causal, window;
@@ -198,6 +199,7 @@ bool mma_supported(int dtype, int D);
 int mma_row_tile(int D, int R);
 int mma_ctas_per_sm(int D, int row_tile);
 int mma_unit_shift(int D);
+int mma_cluster(const FwdParams &p);
 cudaError_t launch_fwd_mma(const FwdParams &p, int kind, cudaStream_t st);
 bool make_tmap_codes(CUtensorMap *m, const void *base, int D, int page, long long heads, int box_rows);
 

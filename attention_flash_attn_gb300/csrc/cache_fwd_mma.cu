@@ -15,6 +15,9 @@
 //   - Q is scaled per row by a power of two into fp16's range: exact for elements within 2^-31 of the
 //     row's largest.
 //   - P is rounded to fp16 (half a step: 2^-11 of each probability, eight times finer than the bf16 result).
+#include <algorithm>
+#include <cmath>
+
 #include "cache_work.cuh"
 #include "tc_common.cuh"
 
@@ -50,7 +53,7 @@ struct Cfg {
   static constexpr size_t Q_BYTES = QREG ? 0 : (size_t)MT * KS * 32 * 16;
   static constexpr size_t ML_BYTES = (size_t)kWarps * ROWS * 8;
   static constexpr size_t NAN_BYTES = (size_t)ROWS * D / 8;  // one bit per output of the run
-  static constexpr size_t SMEM = 1024 + RING + Q_BYTES + ML_BYTES + NAN_BYTES + kWarps * DEPTH * 8;
+  static constexpr size_t SMEM = 1024 + RING + Q_BYTES + ML_BYTES + ROWS * 8 + NAN_BYTES + kWarps * DEPTH * 8;
 };
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int c0, int c1, int c2) {
@@ -58,6 +61,26 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, 
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
+}
+
+// Reads of another cluster CTA's shared memory (`at`: this CTA's address of the same thing).
+__device__ __forceinline__ uint32_t dsmem_at(uint32_t at, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float2 dsmem_f2(uint32_t at, int rank) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(dsmem_at(at, rank)));
+  return v;
+}
+__device__ __forceinline__ float4 dsmem_f4(uint32_t at, int rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(dsmem_at(at, rank)));
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void mma_f16(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
@@ -109,48 +132,57 @@ template <int BLK> __device__ __forceinline__ uint32_t swz(int row, int ch) {
   return row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
 }
 
-// Makes a slice's values fit to be multiplied by P where some row does not see every key: rows of
-// keys that no row sees (slots behind the last token may hold anything) become 0, and e4m3 NaNs too,
-// after the outputs that they belong to -- of the rows that see their key -- are marked in s_nan.  Only a
-// run's first and last slices come here, so it is kept small rather than fast: a key per lane.
-template <int KIND, int D, int MT>
-__device__ __noinline__ void scrub_values(const FwdParams &p, uint8_t *sv, int pos, int key1, unsigned gone, int len, int r0, int rows,
-                                          uint32_t *s_nan, int *s_any) {
-  using C = Cfg<D, MT>;
-  const int lane = threadIdx.x & 31;
-#pragma unroll 1
-  for (int row = lane; row < C::SK; row += 32) {
-    const bool hide = pos + row >= key1 || ((gone >> (row >> 4)) & 1u);
-#pragma unroll 1
-    for (int c = 0; c < D / 16; ++c) {
-      uint8_t *at = sv + (c * 16 / C::BLK) * (C::SK * C::BLK) + swz<C::BLK>(row, c % (C::BLK / 16));
-      uint4 u = lds128(at);
-      uint32_t w[4] = {u.x, u.y, u.z, u.w};
-      bool write = hide;
-      if (hide) {
-        w[0] = w[1] = w[2] = w[3] = 0u;
-      } else if (KIND == ATTN_CACHE_E4M3) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t nan = __vcmpeq4(w[x] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-          if (nan) {
-            write = true;
-#pragma unroll 1
-            for (int r = 0; r < rows; ++r)
-              if (within(row_sees(p, len, query_of(p, r0 + r)), pos + row))
-#pragma unroll 1
-                for (int y = 0; y < 4; ++y)
-                  if ((nan >> (8 * y)) & 1u) {
-                    const int d = c * 16 + x * 4 + y;
-                    atomicOr(s_nan + (r * D + d) / 32, 1u << (d % 32));
-                    *s_any = 1;
-                  }
-            w[x] &= ~nan;
-          }
-        }
+// A 16-byte chunk of values of key `pos` (columns d ..) with e4m3 NaNs in it: the outputs that they belong
+// to -- of the rows that see the key -- are marked in s_nan, and they become 0.
+template <int D>
+__device__ __noinline__ void mark_nans(const FwdParams &p, uint4 *at, int pos, int d, int len, int r0, int rows, uint32_t *s_nan, int *s_any) {
+  uint8_t *code = reinterpret_cast<uint8_t *>(at);
+  for (int x = 0; x < 16; ++x) {
+    if ((code[x] & 0x7f) != 0x7f) continue;
+    code[x] = 0;
+    for (int r = 0; r < rows; ++r)
+      if (within(row_sees(p, len, query_of(p, r0 + r)), pos)) {
+        atomicOr(s_nan + (r * D + d + x) / 32, 1u << ((d + x) % 32));
+        *s_any = 1;
       }
-      if (write) *reinterpret_cast<uint4 *>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// Makes a slice's values fit to be multiplied by P where some row does not see every key: rows of
+// keys that no row sees (slots behind the last token may hold anything) become 0, and so do e4m3 NaNs,
+// whose outputs are marked.  A run's first and last slices come here.
+template <int KIND, int D, int MT>
+__device__ __forceinline__ void scrub_values(const FwdParams &p, uint8_t *sv, int pos, int key1, unsigned gone, int len, int r0, int rows,
+                                             uint32_t *s_nan, int *s_any) {
+  using C = Cfg<D, MT>;
+  constexpr int kChunks = C::SK * D / 16 / 32;  // per lane
+  const int lane = threadIdx.x & 31;
+  auto at = [&](int i, int *row, int *c) {
+    const int x = lane + 32 * i;
+    *row = x / (D / 16);
+    *c = x % (D / 16);
+    return reinterpret_cast<uint4 *>(sv + (*c / (C::BLK / 16)) * (C::SK * C::BLK) + swz<C::BLK>(*row, *c % (C::BLK / 16)));
+  };
+  unsigned nans = 0;
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    int row, c;
+    uint4 *u = at(i, &row, &c);
+    if (pos + row >= key1 || ((gone >> (row >> 4)) & 1u)) {
+      *u = make_uint4(0, 0, 0, 0);
+    } else if (KIND == ATTN_CACHE_E4M3) {
+      const uint4 v = *u;  // a byte of 0x7f, and no other, carries into its top bit
+      const uint32_t any = ((v.x & 0x7f7f7f7fu) + 0x01010101u) | ((v.y & 0x7f7f7f7fu) + 0x01010101u) |
+                           ((v.z & 0x7f7f7f7fu) + 0x01010101u) | ((v.w & 0x7f7f7f7fu) + 0x01010101u);
+      if (any & 0x80808080u) nans |= 1u << i;
     }
+  }
+  while (nans) {
+    const int i = __ffs(nans) - 1;
+    nans &= nans - 1;
+    int row, c;
+    uint4 *u = at(i, &row, &c);
+    mark_nans<D>(p, u, pos + row, c * 16, len, r0, rows, s_nan, s_any);
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the stage's next fill comes by TMA
   __syncwarp();
@@ -167,10 +199,11 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
   uint8_t *base = smem_raw + (ring0 - raw);
   uint4 *s_q = reinterpret_cast<uint4 *>(base + C::RING);                                      // [MT][KS][32]
   float2 *s_ml = reinterpret_cast<float2 *>(base + C::RING + C::Q_BYTES);                      // [kWarps][ROWS]
-  uint32_t *s_nan = reinterpret_cast<uint32_t *>(base + C::RING + C::Q_BYTES + C::ML_BYTES);   // [ROWS][D / 32]
+  float2 *s_cta = s_ml + kWarps * C::ROWS;                                                     // [ROWS]: the CTA's, for its cluster
+  uint32_t *s_nan = reinterpret_cast<uint32_t *>(s_cta + C::ROWS);                             // [ROWS][D / 32]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t ring = ring0 + warp * (C::DEPTH * C::STAGE);
-  const uint32_t bars = ring0 + C::RING + C::Q_BYTES + C::ML_BYTES + C::NAN_BYTES + warp * (C::DEPTH * 8);
+  const uint32_t bars = ring0 + C::RING + C::Q_BYTES + C::ML_BYTES + C::ROWS * 8 + C::NAN_BYTES + warp * (C::DEPTH * 8);
   if (lane == 0) {
 #pragma unroll
     for (int s = 0; s < C::DEPTH; ++s) mbar_init(bars + 8 * s, 1);
@@ -184,11 +217,30 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
 
   __shared__ Groups s_groups;
   Cursor cur;
-  if (!cursor_begin(p, &s_groups, cur)) {
+  Run run;
+  int rank = 0;  // in the item's cluster
+  if (p.cluster) {
+    const int item = blockIdx.x / p.cluster;
+    rank = blockIdx.x - item * p.cluster;
+    run.hk = item / p.NG;
+    const int gr = item - run.hk * p.NG;
+    run.b = p.RT == 1 ? gr : gr / p.RT;
+    run.rt = gr - run.b * p.RT;
+    run.range = group_range(p, run.b, run.rt);
+    run.n = range_units(p, run.range);
+    const int each = run.n / p.cluster, extra = run.n - each * p.cluster;
+    run.off = rank * each + min(rank, extra);
+    run.cnt = each + (rank < extra);
+    if (rank == 0 && run.hk == 0 && run.rt == 0 && tid == 0) {
+      bool bad;
+      seq_len(p.c, run.b, &bad);
+      if (bad) set_status(p.c.status, kStatusBadPage);
+    }
+    __syncthreads();  // s_nan, s_any
+  } else if (!cursor_begin(p, &s_groups, cur) || !cursor_next(p, &s_groups, cur, run)) {
     grid_launch_next();
     return;
   }
-  Run run;
   uint32_t phases = 0;  // parity of each stage's next completion
   int stage = 0;
   bool dead = false;    // a wait gave up: recorded; this warp computes no further
@@ -196,7 +248,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
   int id_nxt[C::NH];
   bool first = true;    // (id_nxt holds the page ids of every run but the first)
 #pragma unroll 1
-  while (cursor_next(p, &s_groups, cur, run)) {
+  do {
     const int r0 = run.rt * C::ROWS, rows = min(C::ROWS, p.R - r0);
     const int key0 = run.range.lo + (run.off << p.unit_shift), key1 = min(run.range.hi, key0 + (run.cnt << p.unit_shift));
     // This warp's slices: key0 + (warp + 4 x) SK for x < n_slices.
@@ -217,7 +269,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
     auto load_next_ids = [&](int batch) {
       if (n_slices > batch * 32 + 32) {
         load_ids(run.b, key0, key1, batch + 1, id_nxt);
-      } else {
+      } else if (!p.cluster) {
         Cursor peek = cur;
         Run next;
         if (cursor_next(p, &s_groups, peek, next)) {
@@ -616,7 +668,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
       stage = stage + 1 == C::DEPTH ? 0 : stage + 1;
     }
 
-    if (cur.u >= cur.u1) grid_launch_next();  // the join's blocks may take up their places
+    if (p.cluster || cur.u >= cur.u1) grid_launch_next();  // the join's blocks may take up their places
 
     // The run's end: each warp leaves its rows in its ring (nothing is in flight), four columns at a time,
     // the 16-byte groups permuted so that the lanes of a store meet different banks; then all threads add
@@ -648,7 +700,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring's next fill comes by TMA
     __syncthreads();
-    const bool whole = run.cnt == run.n, nans = s_any != 0;
+    const bool one_of = p.cluster > 1, whole = !one_of && run.cnt == run.n, nans = s_any != 0;
 #pragma unroll 1
     for (int x = tid; x < rows * (D / 4); x += kThreads) {
       const int r = x / (D / 4), d = (x % (D / 4)) * 4;
@@ -686,18 +738,56 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
         u.x = *reinterpret_cast<uint32_t *>(&a);
         u.y = *reinterpret_cast<uint32_t *>(&b);
         *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.O) + o_row(p, run.b, run.hk, r0 + r) + d) = u;
+      } else if (one_of) {  // into warp 0's place, which this thread alone has read
+        if (d == 0) s_cta[r] = make_float2(M, L);
+        *reinterpret_cast<float4 *>(base + o_at(r, d) * 4) = v;
       } else {
         if (d == 0) p.ml_part[(size_t)run.slot * C::ROWS + r] = make_float2(M, L);
         *reinterpret_cast<float4 *>(p.o_part + ((size_t)run.slot * C::ROWS + r) * D + d) = v;
       }
     }
+    if (one_of) {
+      // The cluster's CTAs share out the item's outputs and add each other's parts up.
+      cluster_sync();
+#pragma unroll 1
+      for (int x = rank * kThreads + tid; x < rows * (D / 4); x += p.cluster * kThreads) {
+        const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+        const uint32_t ml_at = smem_u32(s_cta + r), v_at = smem_u32(base + o_at(r, d) * 4);
+        float M = -CUDART_INF_F, L = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < p.cluster; ++k) {
+          const float2 ml = dsmem_f2(ml_at, k);
+          const float4 u = dsmem_f4(v_at, k);
+          const float top = max_nan(M, ml.x);
+          if (top == -CUDART_INF_F) continue;
+          const float a = ex2(M - top), f = ex2(ml.x - top);
+          M = top;
+          L = L * a + f * ml.y;
+          v.x = v.x * a + f * u.x;
+          v.y = v.y * a + f * u.y;
+          v.z = v.z * a + f * u.z;
+          v.w = v.w * a + f * u.w;
+        }
+        const RowEnd e = row_end(p, run.hk * p.G + (r0 + r) % p.G, M, L);
+        if (d == 0) p.LSE[lse_at(p, run.b, run.hk, r0 + r)] = e.lse;
+        if (M == -CUDART_INF_F) v = make_float4(0.f, 0.f, 0.f, 0.f);
+        __nv_bfloat162 a = __floats2bfloat162_rn(v.x * e.scale, v.y * e.scale), b = __floats2bfloat162_rn(v.z * e.scale, v.w * e.scale);
+        uint2 u;
+        u.x = *reinterpret_cast<uint32_t *>(&a);
+        u.y = *reinterpret_cast<uint32_t *>(&b);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.O) + o_row(p, run.b, run.hk, r0 + r) + d) = u;
+      }
+      cluster_sync();  // no CTA leaves while another reads its part
+    }
+    if (p.cluster) return;
     __syncthreads();  // the ring, s_ml and s_nan are free for the next run
     if (nans) {
       for (int x = tid; x < C::ROWS * D / 32; x += kThreads) s_nan[x] = 0u;
       if (tid == 0) s_any = 0;
       __syncthreads();
     }
-  }
+  } while (cursor_next(p, &s_groups, cur, run));
 }
 
 template <int KIND, int D, int MT>
@@ -712,8 +802,18 @@ cudaError_t launch_t(const FwdParams &p, cudaStream_t st) {
   if (!make_tmap_codes(&km, p.c.k, D, p.c.page, (long long)p.c.num_pages * p.c.Hkv, rows) ||
       !make_tmap_codes(&vm, p.c.v, D, p.c.page, (long long)p.c.num_pages * p.c.Hkv, rows))
     return cudaErrorInvalidValue;
-  kernel<<<p.max_ctas, kThreads, C::SMEM, st>>>(p, km, vm);
-  return counted(cudaGetLastError());
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.cluster ? p.NG * p.c.Hkv * p.cluster : p.max_ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = p.cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+  return counted(cudaLaunchKernelEx(&cfg, kernel, p, km, vm));
 }
 
 template <int KIND> cudaError_t launch_k(const FwdParams &p, cudaStream_t st) {
@@ -737,6 +837,32 @@ int mma_unit_shift(int D) { return D == 64 ? 8 : D == 128 ? 7 : 6; }  // four sl
 
 int mma_ctas_per_sm(int D, int row_tile) {
   return row_tile == 32 || D == 256 ? 2 : 3;  // Cfg's CTAS
+}
+
+// How the work is spread.  A cluster of CTAs for each item (sequence, kv head, row tile) joins its parts in
+// shared memory: one launch, and a CTA has one run.  Splitting all items' keys evenly over one wave of CTAs
+// balances any lengths, at the cost of a plan, of parts through memory and of a second launch.  The host
+// knows the table's width, not the lengths; it takes the cluster size whose waves end first for full
+// rows, in slices of a warp (a slice takes about as long whatever the head dim): kStart for a CTA's start
+// and end, kSplit for the plan and the join.
+int mma_cluster(const FwdParams &p) {
+  constexpr double kStart = 4, kSplit = 6;
+  const long long items = (long long)p.NG * p.c.Hkv;
+  long long keys = (long long)p.c.max_pages << p.c.page_shift;
+  if (p.window > 0) keys = std::min(keys, (long long)p.window + p.Sq);
+  const double units = (double)((keys >> p.unit_shift) + 1);  // a unit: a slice for each warp
+  const double slots = (double)mma_ctas_per_sm(p.c.D, p.row_tile) * device_sm_count();
+  double best = kStart + kSplit + items * units / slots;
+  int cluster = 0;
+  for (int c = 1; c <= 8; c *= 2) {
+    if (items * c > INT_MAX) break;
+    const double waves = std::ceil(items * c / slots), t = waves * (kStart + std::ceil(units / c));
+    if (t < best) {
+      best = t;
+      cluster = c;
+    }
+  }
+  return cluster;
 }
 
 cudaError_t launch_fwd_mma(const FwdParams &p, int kind, cudaStream_t st) {

@@ -109,8 +109,8 @@ int attn_cache_append(const attn_cache *c, const attn_cache_seqs *s, const attn_
  * bf16 queries with D in {64, 128, 256} run on the tensor cores with the codes widened to fp16
  * (exact) and the queries scaled per row by a power of two into fp16 (exact for values within
  * 2^-31 of the row's largest); probabilities are rounded to fp16.  Every other call runs on fp32
- * FFMA kernels.  Long key ranges are split over the grid and joined; how, depends on the
- * lengths alone.
+ * FFMA kernels.  Long key ranges are split over CTAs and joined in a fixed order;
+ * how, depends on the shapes and the lengths alone.
  */
 typedef struct {
     int dtype;                 /* of q and O: enum attn_dtype                             */
