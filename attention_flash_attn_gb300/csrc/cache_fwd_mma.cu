@@ -362,7 +362,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
 #pragma unroll 1
     for (int s = 0; s < min(C::DEPTH, n_slices); ++s) issue(s, stage + s >= C::DEPTH ? stage + s - C::DEPTH : stage + s, id_now);
     fetch_scales();
-    load_next_ids(0);
+    if (n_slices <= 0) load_next_ids(0);
 
     // The queries scaled into fp16.
     uint32_t qf[C::QREG ? MT : 1][C::QREG ? C::KS : 1][4];
@@ -442,12 +442,14 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
 #pragma unroll
         for (int h = 0; h < C::NH; ++h) id_now[h] = id_nxt[h];
         fetch_scales();
-        load_next_ids(x >> 5);
       }
       uint8_t *const sk = base + (warp * C::DEPTH + stage) * C::STAGE, *const sv = sk + C::SK * D;
       if (!dead) dead = !__all_sync(~0u, mbar_wait(bars + 8 * stage, (phases >> stage) & 1u, p.c.status));
       phases ^= 1u << stage;
-      if ((x & 31) == 0) take_scales();
+      if ((x & 31) == 0) {
+        take_scales();
+        load_next_ids(x >> 5);
+      }
       // This slice's scales.
       float ks[C::NH], lv[C::NH];
 #pragma unroll
@@ -840,23 +842,25 @@ int mma_ctas_per_sm(int D, int row_tile) {
 }
 
 // How the work is spread.  A cluster of CTAs for each item (sequence, kv head, row tile) joins its parts in
-// shared memory: one launch, and a CTA has one run.  Splitting all items' keys evenly over one wave of CTAs
-// balances any lengths, at the cost of a plan, of parts through memory and of a second launch.  The host
-// knows the table's width, not the lengths; it takes the cluster size whose waves end first for full
-// rows, in slices of a warp (a slice takes about as long whatever the head dim): kStart for a CTA's start
-// and end, kSplit for the plan and the join.
+// shared memory: one launch, and a CTA has one run, but the longest row decides.  Splitting all items' keys
+// evenly over one wave of CTAs balances any lengths, at the cost of a plan, of parts through memory and of a
+// second launch.  The host knows the table's width, not the lengths: it takes clusters where one wave of
+// them ends before the split would, counted in slices of a warp (1.1 us each, whatever the head dim), full
+// rows against rows half full.  kStart: a CTA's start and end; kSplit: the plan and the join.  Measured (us,
+// cluster / split): 1 x 1531 keys at D = 256 12.4 / 14.4; at D = 128 with 8 kv heads 4 x 2000 12.4 / 14.4,
+// 4 x 8000 22.6 / 24.7, 2 x 16000 31.1 / 24.5 (split taken); clusters in several waves lose (32 x 4000:
+// 53 to 78 / 55; 64 ragged rows at D = 64 46 to 99 / 47).
 int mma_cluster(const FwdParams &p) {
   constexpr double kStart = 4, kSplit = 6;
   const long long items = (long long)p.NG * p.c.Hkv;
   long long keys = (long long)p.c.max_pages << p.c.page_shift;
   if (p.window > 0) keys = std::min(keys, (long long)p.window + p.Sq);
   const double units = (double)((keys >> p.unit_shift) + 1);  // a unit: a slice for each warp
-  const double slots = (double)mma_ctas_per_sm(p.c.D, p.row_tile) * device_sm_count();
-  double best = kStart + kSplit + items * units / slots;
+  const long long slots = (long long)mma_ctas_per_sm(p.c.D, p.row_tile) * device_sm_count();
+  double best = kStart + kSplit + std::ceil(0.5 * items * units / slots);
   int cluster = 0;
-  for (int c = 1; c <= 8; c *= 2) {
-    if (items * c > INT_MAX) break;
-    const double waves = std::ceil(items * c / slots), t = waves * (kStart + std::ceil(units / c));
+  for (int c = 1; c <= 8 && items * c <= slots; c *= 2) {
+    const double t = kStart + std::ceil(units / c);
     if (t < best) {
       best = t;
       cluster = c;
