@@ -99,7 +99,7 @@ int validate(const attn_cache *c, const attn_cache_seqs *s, const attn_cache_fwd
   return ATTN_OK;
 }
 
-bool use_mma(const attn_cache *c, const attn_cache_fwd_args *a) { return mma_supported(a->dtype, c->D); }
+bool use_mma(const attn_cache *c) { return mma_supported(c->D); }
 
 struct FwdLayout {
   size_t prefix, o_part, ml_part, scores, total;
@@ -113,8 +113,8 @@ FwdParams fwd_params(const attn_cache *c, const attn_cache_seqs *s, const attn_c
   p.Hq = a->Hq;
   p.G = a->Hq / c->Hkv;
   p.R = p.G * a->Sq;
-  const bool mma = use_mma(c, a);
-  p.row_tile = mma ? mma_row_tile(c->D, p.R) : simt_row_tile();
+  const bool mma = use_mma(c);
+  p.row_tile = mma ? mma_row_tile(a->dtype, c->D, p.R) : simt_row_tile();
   p.RT = (p.R + p.row_tile - 1) / p.row_tile;
   p.NG = s->B * p.RT;
   const long long cap = (long long)s->max_pages * c->page_size;
@@ -204,7 +204,7 @@ size_t attn_cache_fwd_workspace_size(const attn_cache *c, const attn_cache_seqs 
 
 const char *attn_cache_path_name(const attn_cache *c, const attn_cache_seqs *s, const attn_cache_fwd_args *a) {
   if (validate(c, s, a) != ATTN_OK) return "";
-  return use_mma(c, a) ? "mma" : "simt";
+  return use_mma(c) ? "mma" : "simt";
 }
 
 int attn_cache_fwd(const attn_cache *c, const attn_cache_seqs *s, const attn_cache_fwd_args *a, void *O,
@@ -224,7 +224,7 @@ int attn_cache_fwd(const attn_cache *c, const attn_cache_seqs *s, const attn_cac
   p.O = O;
   p.LSE = LSE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = use_mma(c, a) ? launch_fwd_mma(p, c->kind, st) : launch_fwd_simt(p, a->dtype, c->kind, st);
+  cudaError_t e = use_mma(c) ? launch_fwd_mma(p, a->dtype, c->kind, st) : launch_fwd_simt(p, a->dtype, c->kind, st);
   if (e == cudaSuccess && !p.cluster) e = launch_fwd_join(p, a->dtype, st);
   if (e == cudaSuccess && a->weights && s->max_pages > 0) e = launch_weights(p, st);
   return cuda_status(e);

@@ -195,12 +195,14 @@ int simt_row_tile();
 int simt_unit_shift();
 
 // Tensor-core path.
-bool mma_supported(int dtype, int D);
-int mma_row_tile(int D, int R);
+bool mma_supported(int D);
+int mma_row_tile(int dtype, int D, int R);
 int mma_ctas_per_sm(int D, int row_tile);
 int mma_unit_shift(int D);
 int mma_cluster(const FwdParams &p);
-cudaError_t launch_fwd_mma(const FwdParams &p, int kind, cudaStream_t st);
+cudaError_t launch_fwd_mma(const FwdParams &p, int dtype, int kind, cudaStream_t st);
+cudaError_t launch_mma_e4m3(const FwdParams &p, int dtype, cudaStream_t st);
+cudaError_t launch_mma_int8(const FwdParams &p, int dtype, cudaStream_t st);
 bool make_tmap_codes(CUtensorMap *m, const void *base, int D, int page, long long heads, int box_rows);
 
 cudaError_t launch_fwd_join(const FwdParams &p, int dtype, cudaStream_t st);

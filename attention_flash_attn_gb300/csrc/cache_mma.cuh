@@ -1,5 +1,5 @@
-// cache_fwd_mma.cu -- attention over the 8-bit cache on the tensor cores: bf16 queries, head dims 64,
-// 128 and 256.
+// cache_mma.cuh -- attention over the 8-bit cache on the tensor cores, head dims 64, 128 and 256
+// (instantiated for each kind of code in its own file).
 //
 // Decoding reads 2 D bytes of codes per key and kv head and does 4 D flops per byte and query row, so
 // with the few rows of a step (G heads share a kv head) it is bound by memory; what can keep it from
@@ -15,9 +15,10 @@
 //   - Q is scaled per row by a power of two into fp16's range: exact for elements within 2^-31 of the
 //     row's largest.
 //   - P is rounded to fp16 (half a step: 2^-11 of each probability, eight times finer than the bf16 result).
-#include <algorithm>
-#include <cmath>
-
+//   - float queries take the same way in two terms each: q = hi + lo in fp16 (22 bits), p 2^14 = hi + lo, both
+//     terms multiplied into the same accumulators.  Twice the MMAs, which the memory hides; the fp32 pipes
+//     alone took 39 us where this takes 14 (9 ragged rows up to 9001 keys, one kv head).
+#pragma once
 #include "cache_work.cuh"
 #include "tc_common.cuh"
 
@@ -30,9 +31,11 @@ using namespace attn::tc;
 constexpr int kWarps = kThreads / 32;
 constexpr float kZeroLog = kMinScaleExp - 1;
 
-template <int D_, int MT_>
+template <typename T, int D_, int MT_>
 struct Cfg {
   static constexpr int D = D_, MT = MT_;
+  static constexpr int TERMS = sizeof(T) == 4 ? 2 : 1;  // fp16 terms of a query element and of a probability
+  static constexpr int PSHIFT = sizeof(T) == 4 ? 14 : 0;  // probabilities are held times 2^PSHIFT: two terms without subnormals
   static constexpr int SK = D == 256 ? 16 : D == 128 ? 32 : 64;  // keys of a slice: 8 KB of codes
   static constexpr int NH = SK / 16;                   // groups of 16 keys: each lies in one page
   static constexpr int BLK = D < 128 ? D : 128;        // columns of one TMA box row
@@ -45,12 +48,12 @@ struct Cfg {
   static constexpr int STAGE = 2 * SK * D;             // bytes of a slice, K then V
   static constexpr int DEPTH = 2;
   static constexpr int CTAS = MT == 1 && D <= 128 ? 3 : 2;
-  static constexpr bool QREG = D * MT <= 64;           // Q fragments in registers, else in shared memory
+  static constexpr bool QREG = D * MT * TERMS <= 64;   // Q fragments in registers, else in shared memory
   static constexpr int ROWS = 16 * MT;
   static_assert(NB == 1 || NH == 1, "a slice of several pages has one box per page");
   static constexpr size_t RING = (size_t)kWarps * DEPTH * STAGE;
   static_assert(DEPTH * STAGE >= ROWS * D * 4, "a warp's output fits its ring at the end of a run");
-  static constexpr size_t Q_BYTES = QREG ? 0 : (size_t)MT * KS * 32 * 16;
+  static constexpr size_t Q_BYTES = QREG ? 0 : (size_t)TERMS * MT * KS * 32 * 16;
   static constexpr size_t ML_BYTES = (size_t)kWarps * ROWS * 8;
   static constexpr size_t NAN_BYTES = (size_t)ROWS * D / 8;  // one bit per output of the run
   static constexpr size_t SMEM = 1024 + RING + Q_BYTES + ML_BYTES + ROWS * 8 + NAN_BYTES + kWarps * DEPTH * 8;
@@ -104,6 +107,28 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   return r;
 }
 
+// What a pair in fp16 leaves of the values it was rounded from, in fp16 (0 where they are not finite, so
+// that the sum is what it would be without).
+__device__ __forceinline__ uint32_t rest_h2(uint32_t h, float lo, float hi) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+  const float a = lo - f.x, b = hi - f.y;
+  return pack_h2(fabsf(a) <= 3.402823466e38f ? a : 0.f, fabsf(b) <= 3.402823466e38f ? b : 0.f);
+}
+
+// Elements x and x + 1 (x even) of a lane's part of a query row.
+template <typename T> __device__ __forceinline__ void q_pair(const uint4 *raw, int x, float &a, float &b) {
+  if (sizeof(T) == 4) {
+    const uint4 &u = raw[x / 4];
+    a = __uint_as_float(x % 4 ? u.z : u.x);
+    b = __uint_as_float(x % 4 ? u.w : u.y);
+  } else {
+    const uint4 &u = raw[x / 8];
+    const uint32_t w = x % 8 == 0 ? u.x : x % 8 == 2 ? u.y : x % 8 == 4 ? u.z : u.w;
+    a = __uint_as_float(w << 16);
+    b = __uint_as_float(w & 0xffff0000u);
+  }
+}
+
 // Four codes of a word widened to two fp16 pairs, exactly.  int8: code + 128 under the bits of 1024
 // is 1152 + code in fp16.
 template <int KIND> __device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
@@ -124,6 +149,12 @@ template <int KIND> __device__ __forceinline__ void widen4(uint32_t w, uint32_t 
 // steps of the cap; saturates cleanly (2^y = inf gives 1, 0 gives -1).
 __device__ __forceinline__ float softcap_log2(float y, float cap_log2) {
   return cap_log2 - __fdividef(2.f * cap_log2, 1.f + ex2(y));
+}
+
+__device__ __forceinline__ void put4(float *p, float4 x) { *reinterpret_cast<float4 *>(p) = x; }
+__device__ __forceinline__ void put4(__nv_bfloat16 *p, float4 x) {
+  __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+  *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<uint32_t *>(&a), *reinterpret_cast<uint32_t *>(&b));
 }
 
 // Byte offset of 16-byte chunk `ch` of key row `row` in a box, under TMA's swizzle.
@@ -151,10 +182,10 @@ __device__ __noinline__ void mark_nans(const FwdParams &p, uint4 *at, int pos, i
 // Makes a slice's values fit to be multiplied by P where some row does not see every key: rows of
 // keys that no row sees (slots behind the last token may hold anything) become 0, and so do e4m3 NaNs,
 // whose outputs are marked.  A run's first and last slices come here.
-template <int KIND, int D, int MT>
+template <typename T, int KIND, int D, int MT>
 __device__ __forceinline__ void scrub_values(const FwdParams &p, uint8_t *sv, int pos, int key1, unsigned gone, int len, int r0, int rows,
                                              uint32_t *s_nan, int *s_any) {
-  using C = Cfg<D, MT>;
+  using C = Cfg<T, D, MT>;
   constexpr int kChunks = C::SK * D / 16 / 32;  // per lane
   const int lane = threadIdx.x & 31;
   auto at = [&](int i, int *row, int *c) {
@@ -188,16 +219,16 @@ __device__ __forceinline__ void scrub_values(const FwdParams &p, uint8_t *sv, in
   __syncwarp();
 }
 
-template <int KIND, int D, int MT>
-__global__ void __launch_bounds__(kThreads, (Cfg<D, MT>::CTAS))
+template <typename T, int KIND, int D, int MT>
+__global__ void __launch_bounds__(kThreads, (Cfg<T, D, MT>::CTAS))
 cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
-  using C = Cfg<D, MT>;
+  using C = Cfg<T, D, MT>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int s_any;
   const uint32_t raw = smem_u32(smem_raw), ring0 = (raw + 1023u) & ~1023u;
   uint8_t *base = smem_raw + (ring0 - raw);
-  uint4 *s_q = reinterpret_cast<uint4 *>(base + C::RING);                                      // [MT][KS][32]
+  uint4 *s_q = reinterpret_cast<uint4 *>(base + C::RING);                                      // [TERMS][MT][KS][32]
   float2 *s_ml = reinterpret_cast<float2 *>(base + C::RING + C::Q_BYTES);                      // [kWarps][ROWS]
   float2 *s_cta = s_ml + kWarps * C::ROWS;                                                     // [ROWS]: the CTA's, for its cluster
   uint32_t *s_nan = reinterpret_cast<uint32_t *>(s_cta + C::ROWS);                             // [ROWS][D / 32]
@@ -341,17 +372,19 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
     };
 
     // Queries: rows g and g + 8 of each 16, this lane's columns; asked for before anything that waits.
-    uint4 raw_q[MT][2][D / 32];
+    constexpr int kQW = D * (int)sizeof(T) / 64;  // 16-byte words of a row's quarter
+    uint4 raw_q[MT][2][kQW];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int r = r0 + mt * 16 + 8 * y + g, i = query_of(p, r), h = run.hk * p.G + (r - i * p.G);
-        const __nv_bfloat16 *row = static_cast<const __nv_bfloat16 *>(p.q) + run.b * p.q_sb + i * p.q_ss + h * p.q_sh + t * (C::BLK / 4);
+        const T *row = static_cast<const T *>(p.q) + run.b * p.q_sb + i * p.q_ss + h * p.q_sh + t * (C::BLK / 4);
 #pragma unroll
-        for (int z = 0; z < D / 32; ++z) {
+        for (int z = 0; z < kQW; ++z) {
+          constexpr int kPerBlk = kQW / C::NB, kEl = 16 / (int)sizeof(T);
           raw_q[mt][y][z] = make_uint4(0, 0, 0, 0);
-          if (r < p.R) raw_q[mt][y][z] = *reinterpret_cast<const uint4 *>(row + (z / (C::BLK / 32)) * C::BLK + (z % (C::BLK / 32)) * 8);
+          if (r < p.R) raw_q[mt][y][z] = *reinterpret_cast<const uint4 *>(row + (z / kPerBlk) * C::BLK + (z % kPerBlk) * kEl);
         }
       }
 
@@ -370,6 +403,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
     int see_lo[MT][2], see_n[MT][2];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
+      float up[2];
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int2 see = row_sees(p, run.range.len, query_of(p, r0 + mt * 16 + 8 * y + g));
@@ -377,11 +411,10 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
         see_n[mt][y] = max(0, min(see.y, key1) - see.x);
         float amax = 0.f;
 #pragma unroll
-        for (int z = 0; z < D / 32; ++z) {
-          const uint32_t w[4] = {raw_q[mt][y][z].x, raw_q[mt][y][z].y, raw_q[mt][y][z].z, raw_q[mt][y][z].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            amax = max_nan(amax, max_nan(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+        for (int x = 0; x < D / 4; x += 2) {
+          float q0, q1;
+          q_pair<T>(raw_q[mt][y], x, q0, q1);
+          amax = max_nan(amax, fabsf(q0), fabsf(q1));
         }
         amax = max_nan(amax, __shfl_xor_sync(~0u, amax, 1));
         amax = max_nan(amax, __shfl_xor_sync(~0u, amax, 2));
@@ -389,30 +422,32 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
         int x = 14 - ((int)(__float_as_uint(amax) >> 23) - 127);
         if (!(amax > 0.f) || !(amax <= 3.402823466e38f)) x = 0;
         x = x > 126 ? 126 : x;
-        const float up = copysignf(__uint_as_float((unsigned)(x + 127) << 23), p.scale);
-        q_mul[mt][y] = __uint_as_float((unsigned)(127 - x) << 23) * fabsf(p.scale) * (p.cap > 0.f ? 2.f * kLog2e * p.inv_cap : kLog2e);
-#pragma unroll
-        for (int z = 0; z < D / 32; ++z) {
-          uint4 &u = raw_q[mt][y][z];
-          uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = pack_h2(__uint_as_float(w[e] << 16) * up, __uint_as_float(w[e] & 0xffff0000u) * up);
-          u = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        up[y] = copysignf(__uint_as_float((unsigned)(x + 127) << 23), p.scale);
+        // (The capped logit's argument: of 2^y for bf16, see softcap_log2, of tanh for float.)
+        const float unit = p.cap > 0.f ? (C::TERMS == 1 ? 2.f * kLog2e * p.inv_cap : p.inv_cap) : kLog2e;
+        q_mul[mt][y] = __uint_as_float((unsigned)(127 - x) << 23) * fabsf(p.scale) * unit;
       }
-      // A fragment of k-step s: columns 4 s .. 4 s + 3 of this lane's (words 2 s and 2 s + 1).
+      // A fragment of k-step s: columns 4 s .. 4 s + 3 of this lane's, of rows g and g + 8.
 #pragma unroll
       for (int s = 0; s < C::KS; ++s) {
-        const uint4 &u = raw_q[mt][0][s / 2], &v = raw_q[mt][1][s / 2];
-        const uint4 f = s % 2 ? make_uint4(u.z, v.z, u.w, v.w) : make_uint4(u.x, v.x, u.y, v.y);
-        if (C::QREG) {
-          qf[C::QREG ? mt : 0][C::QREG ? s : 0][0] = f.x;
-          qf[C::QREG ? mt : 0][C::QREG ? s : 0][1] = f.y;
-          qf[C::QREG ? mt : 0][C::QREG ? s : 0][2] = f.z;
-          qf[C::QREG ? mt : 0][C::QREG ? s : 0][3] = f.w;
-        } else if (warp == 0) {
-          s_q[(mt * C::KS + s) * 32 + lane] = f;
+        uint32_t f[C::TERMS][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float q0, q1;
+          q_pair<T>(raw_q[mt][e & 1], 4 * s + 2 * (e >> 1), q0, q1);
+          q0 *= up[e & 1];
+          q1 *= up[e & 1];
+          f[0][e] = pack_h2(q0, q1);
+          if (C::TERMS == 2) f[C::TERMS - 1][e] = rest_h2(f[0][e], q0, q1);
+        }
+#pragma unroll
+        for (int w = 0; w < C::TERMS; ++w) {
+          if (C::QREG) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) qf[C::QREG ? mt : 0][C::QREG ? s : 0][e] = f[w][e];
+          } else if (warp == 0) {
+            s_q[((w * MT + mt) * C::KS + s) * 32 + lane] = make_uint4(f[w][0], f[w][1], f[w][2], f[w][3]);
+          }
         }
       }
     }
@@ -481,24 +516,28 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
 #pragma unroll
               for (int w = 0; w < 4; ++w) {
                 const int step = (j * C::CH + c) * 4 + w;
-                uint4 qs[MT];
+                uint4 qs[C::TERMS][MT];
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                  if (!C::QREG) qs[mt] = s_q[(mt * C::KS + step) * 32 + lane];
+                for (int z = 0; z < C::TERMS; ++z)
+#pragma unroll
+                  for (int mt = 0; mt < MT; ++mt)
+                    if (!C::QREG) qs[z][mt] = s_q[((z * MT + mt) * C::KS + step) * 32 + lane];
 #pragma unroll
                 for (int n = 0; n < C::QG; ++n) {
                   const uint32_t word = w == 0 ? kw[n].x : w == 1 ? kw[n].y : w == 2 ? kw[n].z : kw[n].w;
                   uint32_t b0, b1;
                   widen4<KIND>(word, b0, b1);
 #pragma unroll
-                  for (int mt = 0; mt < MT; ++mt) {
-                    if (C::QREG) {
-                      mma_f16(s[mt][n0 + n], qf[C::QREG ? mt : 0][C::QREG ? step : 0], b0, b1);
-                    } else {
-                      const uint32_t a[4] = {qs[mt].x, qs[mt].y, qs[mt].z, qs[mt].w};
-                      mma_f16(C::SPLIT && (w & 1) ? s2[mt][C::SPLIT ? n0 + n : 0] : s[mt][n0 + n], a, b0, b1);
+                  for (int z = 0; z < C::TERMS; ++z)
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                      if (C::QREG) {
+                        mma_f16(s[mt][n0 + n], qf[C::QREG ? mt : 0][C::QREG ? step : 0], b0, b1);
+                      } else {
+                        const uint32_t a[4] = {qs[z][mt].x, qs[z][mt].y, qs[z][mt].z, qs[z][mt].w};
+                        mma_f16(C::SPLIT && (w & 1) ? s2[mt][C::SPLIT ? n0 + n : 0] : s[mt][n0 + n], a, b0, b1);
+                      }
                     }
-                  }
                 }
               }
             }
@@ -533,7 +572,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
 #pragma unroll
               for (int n = 0; n < C::SK / 8; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[mt][n][e] = softcap_log2(s[mt][n][e], cap_log2);
+                for (int e = 0; e < 4; ++e) s[mt][n][e] = C::TERMS == 1 ? softcap_log2(s[mt][n][e], cap_log2) : cap_log2 * tanhf(s[mt][n][e]);
           }
           if (partial) {
             unsigned gone = 0, zero = 0;  // bit h: half h has no page; its values count as 0
@@ -552,7 +591,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
                   if ((gone >> (n / 2) & 1u) || (unsigned)(key - see_lo[mt][e >> 1]) >= (unsigned)see_n[mt][e >> 1])
                     s[mt][n][e] = -CUDART_INF_F;
                 }
-            scrub_values<KIND, D, MT>(p, sv, pos, key1, gone | zero, run.range.len, r0, rows, s_nan, &s_any);
+            scrub_values<T, KIND, D, MT>(p, sv, pos, key1, gone | zero, run.range.len, r0, rows, s_nan, &s_any);
           }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
@@ -574,7 +613,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
                       make_float2(f[mt][y][n / 2] * s[mt][n][2 * y], f[mt][y][n / 2] * s[mt][n][2 * y + 1]);
               }
         }
-        uint32_t pf[MT][C::NH][4];
+        uint32_t pf[C::TERMS][MT][C::NH][4];
         bool moved = false;
         float mn[MT][2];
 #pragma unroll
@@ -615,13 +654,17 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              const float ref = lv[h] - (m[mt][y] == -CUDART_INF_F ? 0.f : m[mt][y]);
+              const float ref = lv[h] - (m[mt][y] == -CUDART_INF_F ? 0.f : m[mt][y]) + (float)C::PSHIFT;
               float e[4];
 #pragma unroll
               for (int q = 0; q < 4; ++q) e[q] = ex2(fmaf(f[mt][y][h], s[mt][2 * h + (q >> 1)][2 * y + (q & 1)], ref));
               l[mt][y] = fmaf((e[0] + e[1]) + (e[2] + e[3]), inv, l[mt][y]);
-              pf[mt][h][y] = pack_h2(e[0], e[1]);
-              pf[mt][h][2 + y] = pack_h2(e[2], e[3]);
+              pf[0][mt][h][y] = pack_h2(e[0], e[1]);
+              pf[0][mt][h][2 + y] = pack_h2(e[2], e[3]);
+              if (C::TERMS == 2) {
+                pf[C::TERMS - 1][mt][h][y] = rest_h2(pf[0][mt][h][y], e[0], e[1]);
+                pf[C::TERMS - 1][mt][h][2 + y] = rest_h2(pf[0][mt][h][2 + y], e[2], e[3]);
+              }
             }
         }
         // O += P V: lane t has keys 2t, 2t + 1, 2t + 8, 2t + 9 of each 16 as the B operand's rows, and
@@ -658,7 +701,9 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
-                  for (int mt = 0; mt < MT; ++mt) mma_f16(o[mt][j * (C::BLK / 8) + 4 * w + 2 * z + e], pf[mt][h], b0[e], b1[e]);
+                  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int q = 0; q < C::TERMS; ++q) mma_f16(o[mt][j * (C::BLK / 8) + 4 * w + 2 * z + e], pf[q][mt][h], b0[e], b1[e]);
               }
           }
       }
@@ -688,7 +733,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
           float v = l[mt][y];
           v += __shfl_xor_sync(~0u, v, 1);
           v += __shfl_xor_sync(~0u, v, 2);
-          if (t == 0) s_ml[warp * C::ROWS + r] = make_float2(m[mt][y], dead ? CUDART_NAN_F : v);
+          if (t == 0) s_ml[warp * C::ROWS + r] = make_float2(m[mt][y] - (float)C::PSHIFT, dead ? CUDART_NAN_F : v);
 #pragma unroll
           for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -735,11 +780,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
       if (whole) {
         const RowEnd e = row_end(p, run.hk * p.G + (r0 + r) % p.G, M, L);
         if (d == 0) p.LSE[lse_at(p, run.b, run.hk, r0 + r)] = e.lse;
-        __nv_bfloat162 a = __floats2bfloat162_rn(v.x * e.scale, v.y * e.scale), b = __floats2bfloat162_rn(v.z * e.scale, v.w * e.scale);
-        uint2 u;
-        u.x = *reinterpret_cast<uint32_t *>(&a);
-        u.y = *reinterpret_cast<uint32_t *>(&b);
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.O) + o_row(p, run.b, run.hk, r0 + r) + d) = u;
+        put4(static_cast<T *>(p.O) + o_row(p, run.b, run.hk, r0 + r) + d, make_float4(v.x * e.scale, v.y * e.scale, v.z * e.scale, v.w * e.scale));
       } else if (one_of) {  // into warp 0's place, which this thread alone has read
         if (d == 0) s_cta[r] = make_float2(M, L);
         *reinterpret_cast<float4 *>(base + o_at(r, d) * 4) = v;
@@ -774,11 +815,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
         const RowEnd e = row_end(p, run.hk * p.G + (r0 + r) % p.G, M, L);
         if (d == 0) p.LSE[lse_at(p, run.b, run.hk, r0 + r)] = e.lse;
         if (M == -CUDART_INF_F) v = make_float4(0.f, 0.f, 0.f, 0.f);
-        __nv_bfloat162 a = __floats2bfloat162_rn(v.x * e.scale, v.y * e.scale), b = __floats2bfloat162_rn(v.z * e.scale, v.w * e.scale);
-        uint2 u;
-        u.x = *reinterpret_cast<uint32_t *>(&a);
-        u.y = *reinterpret_cast<uint32_t *>(&b);
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.O) + o_row(p, run.b, run.hk, r0 + r) + d) = u;
+        put4(static_cast<T *>(p.O) + o_row(p, run.b, run.hk, r0 + r) + d, make_float4(v.x * e.scale, v.y * e.scale, v.z * e.scale, v.w * e.scale));
       }
       cluster_sync();  // no CTA leaves while another reads its part
     }
@@ -792,10 +829,10 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
   } while (cursor_next(p, &s_groups, cur, run));
 }
 
-template <int KIND, int D, int MT>
+template <typename T, int KIND, int D, int MT>
 cudaError_t launch_t(const FwdParams &p, cudaStream_t st) {
-  using C = Cfg<D, MT>;
-  auto kernel = cache_fwd_mma_kernel<KIND, D, MT>;
+  using C = Cfg<T, D, MT>;
+  auto kernel = cache_fwd_mma_kernel<T, KIND, D, MT>;
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = raise_smem(kernel, done, C::SMEM);
   if (e != cudaSuccess) return e;
@@ -818,60 +855,22 @@ cudaError_t launch_t(const FwdParams &p, cudaStream_t st) {
   return counted(cudaLaunchKernelEx(&cfg, kernel, p, km, vm));
 }
 
-template <int KIND> cudaError_t launch_k(const FwdParams &p, cudaStream_t st) {
+template <int KIND> cudaError_t launch_kind(const FwdParams &p, int dtype, cudaStream_t st) {
+  if (dtype == kF32) {
+    switch (p.c.D) {
+      case 64: return launch_t<float, KIND, 64, 1>(p, st);
+      case 128: return launch_t<float, KIND, 128, 1>(p, st);
+      default: return launch_t<float, KIND, 256, 1>(p, st);
+    }
+  }
   const bool two = p.row_tile == 32;
   switch (p.c.D) {
-    case 64: return two ? launch_t<KIND, 64, 2>(p, st) : launch_t<KIND, 64, 1>(p, st);
-    case 128: return two ? launch_t<KIND, 128, 2>(p, st) : launch_t<KIND, 128, 1>(p, st);
-    default: return launch_t<KIND, 256, 1>(p, st);
+    case 64: return two ? launch_t<__nv_bfloat16, KIND, 64, 2>(p, st) : launch_t<__nv_bfloat16, KIND, 64, 1>(p, st);
+    case 128: return two ? launch_t<__nv_bfloat16, KIND, 128, 2>(p, st) : launch_t<__nv_bfloat16, KIND, 128, 1>(p, st);
+    default: return launch_t<__nv_bfloat16, KIND, 256, 1>(p, st);
   }
 }
 
 }  // namespace
-
-bool mma_supported(int dtype, int D) { return dtype == kBF16 && (D == 64 || D == 128 || D == 256); }
-
-// Rows of a work item: 16, or 32 where there are more rows than that and the accumulators fit
-// (head dims up to 128), so that widening a code serves two row tiles.
-int mma_row_tile(int D, int R) { return R > 16 && D <= 128 ? 32 : 16; }
-
-int mma_unit_shift(int D) { return D == 64 ? 8 : D == 128 ? 7 : 6; }  // four slices
-
-int mma_ctas_per_sm(int D, int row_tile) {
-  return row_tile == 32 || D == 256 ? 2 : 3;  // Cfg's CTAS
-}
-
-// How the work is spread.  A cluster of CTAs for each item (sequence, kv head, row tile) joins its parts in
-// shared memory: one launch, and a CTA has one run, but the longest row decides.  Splitting all items' keys
-// evenly over one wave of CTAs balances any lengths, at the cost of a plan, of parts through memory and of a
-// second launch.  The host knows the table's width, not the lengths: it takes clusters where one wave of
-// them ends before the split would, counted in slices of a warp (1.1 us each, whatever the head dim), full
-// rows against rows half full.  kStart: a CTA's start and end; kSplit: the plan and the join.  Measured (us,
-// cluster / split): 1 x 1531 keys at D = 256 12.4 / 14.4; at D = 128 with 8 kv heads 4 x 2000 12.4 / 14.4,
-// 4 x 8000 22.6 / 24.7, 2 x 16000 31.1 / 24.5 (split taken); clusters in several waves lose (32 x 4000:
-// 53 to 78 / 55; 64 ragged rows at D = 64 46 to 99 / 47).
-int mma_cluster(const FwdParams &p) {
-  constexpr double kStart = 4, kSplit = 6;
-  const long long items = (long long)p.NG * p.c.Hkv;
-  long long keys = (long long)p.c.max_pages << p.c.page_shift;
-  if (p.window > 0) keys = std::min(keys, (long long)p.window + p.Sq);
-  const double units = (double)((keys >> p.unit_shift) + 1);  // a unit: a slice for each warp
-  const long long slots = (long long)mma_ctas_per_sm(p.c.D, p.row_tile) * device_sm_count();
-  double best = kStart + kSplit + std::ceil(0.5 * items * units / slots);
-  int cluster = 0;
-  for (int c = 1; c <= 8 && items * c <= slots; c *= 2) {
-    const double t = kStart + std::ceil(units / c);
-    if (t < best) {
-      best = t;
-      cluster = c;
-    }
-  }
-  return cluster;
-}
-
-cudaError_t launch_fwd_mma(const FwdParams &p, int kind, cudaStream_t st) {
-  return kind == ATTN_CACHE_E4M3 ? launch_k<ATTN_CACHE_E4M3>(p, st) : launch_k<ATTN_CACHE_INT8>(p, st);
-}
-
 }  // namespace cache
 }  // namespace attn

@@ -106,10 +106,10 @@ int attn_cache_append(const attn_cache *c, const attn_cache_seqs *s, const attn_
  * in float, summed in a fixed order (no atomics).  weights == weights_out adds in place; both
  * are [B, Hkv, >= max_pages * page_size] with the same element strides.
  *
- * bf16 queries with D in {64, 128, 256} run on the tensor cores with the codes widened to fp16
- * (exact) and the queries scaled per row by a power of two into fp16 (exact for values within
- * 2^-31 of the row's largest); probabilities are rounded to fp16.  Every other call runs on fp32
- * FFMA kernels.  Long key ranges are split over CTAs and joined in a fixed order;
+ * Head dims 64, 128 and 256 run on the tensor cores with the codes widened to fp16 (exact) and the
+ * queries scaled per row by a power of two into fp16: bf16 queries exactly (elements within 2^-31
+ * of the row's largest) with probabilities rounded to fp16, float queries and their
+ * probabilities in two fp16 terms (22 bits).  Other head dims run on fp32 FFMA kernels.  Long key ranges are split over CTAs and joined in a fixed order;
  * how, depends on the shapes and the lengths alone.
  */
 typedef struct {
