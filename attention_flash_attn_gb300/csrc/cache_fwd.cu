@@ -354,30 +354,45 @@ __global__ void __launch_bounds__(kThreads) cache_join_kernel(const __grid_const
 }
 
 // weights_out = weights + sum over the rows of 2^(score - LSE): four keys per thread, the rows'
-// scores read as the attention kernel stored them, summed in row order.
+// scores read as the attention kernel stored them, four rows at a time (loads before sums: bound by
+// the latency of each otherwise), summed in row order.
 __global__ void __launch_bounds__(kThreads) cache_weights_kernel(const __grid_constant__ FwdParams p) {
-  grid_wait();
   const int b = blockIdx.x / p.c.Hkv, hk = blockIdx.x - b * p.c.Hkv;
   const int len = seq_len(p.c, b);
   const int j0 = (blockIdx.y * kThreads + threadIdx.x) * 4;
-  if (j0 >= len) return;
-  float w[4] = {0.f, 0.f, 0.f, 0.f};
-  const float *row = scores_row(p, b, hk, 0) + j0;
-  for (int r = 0; r < p.R; ++r, row += p.Lpad) {
-    // Scores are stored for the keys that some row of the tile sees (a superset of these).
-    const int2 see = row_sees(p, len, query_of(p, r));
-    if (j0 >= see.y || j0 + 3 < see.x) continue;
-    const float lse2 = p.LSE[lse_at(p, b, hk, r)] * kLog2e;
-    const float4 s = *reinterpret_cast<const float4 *>(row);
-    const float t[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-      if (within(see, j0 + x)) w[x] += t[x] == -CUDART_INF_F ? 0.f : exp2f(t[x] - lse2);
-  }
   const size_t at = (size_t)b * p.w_sb + (size_t)hk * p.w_sh + j0;
+  float w[4] = {0.f, 0.f, 0.f, 0.f}, sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int x = 0; x < 4; ++x)
-    if (j0 + x < len) p.w_out[at + x] = p.w_in[at + x] + w[x];
+    if (j0 + x < len) w[x] = p.w_in[at + x];
+  grid_wait();
+  if (j0 >= len) return;
+  const float *row = scores_row(p, b, hk, 0) + j0;
+#pragma unroll 1
+  for (int r0 = 0; r0 < p.R; r0 += 4, row += 4 * p.Lpad) {
+    // Scores are stored for the keys that some row of the tile sees (a superset of what a row sees).
+    int2 see[4];
+    float lse2[4];
+    float4 s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = min(r0 + i, p.R - 1);
+      see[i] = r0 + i < p.R ? row_sees(p, len, query_of(p, r)) : make_int2(0, 0);
+      const bool some = j0 < see[i].y && j0 + 3 >= see[i].x;
+      lse2[i] = some ? p.LSE[lse_at(p, b, hk, r)] * kLog2e : 0.f;
+      s[i] = some ? *reinterpret_cast<const float4 *>(row + i * p.Lpad) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float t[4] = {s[i].x, s[i].y, s[i].z, s[i].w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (within(see[i], j0 + x)) sum[x] += t[x] == -CUDART_INF_F ? 0.f : exp2f(t[x] - lse2[i]);
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+    if (j0 + x < len) p.w_out[at + x] = w[x] + sum[x];
 }
 
 template <typename T, int KIND>
