@@ -99,6 +99,9 @@ int validate(const attn_cache *c, const attn_cache_seqs *s, const attn_cache_fwd
   return ATTN_OK;
 }
 
+bool use_tc(const attn_cache *c, const attn_cache_fwd_args *a) {
+  return tc_supported_rows(a->dtype, c->D, a->Hq / c->Hkv * a->Sq);
+}
 bool use_mma(const attn_cache *c) { return mma_supported(c->D); }
 
 struct FwdLayout {
@@ -113,12 +116,12 @@ FwdParams fwd_params(const attn_cache *c, const attn_cache_seqs *s, const attn_c
   p.Hq = a->Hq;
   p.G = a->Hq / c->Hkv;
   p.R = p.G * a->Sq;
-  const bool mma = use_mma(c);
-  p.row_tile = mma ? mma_row_tile(a->dtype, c->D, p.R) : simt_row_tile();
+  const bool tc = use_tc(c, a), mma = !tc && use_mma(c);
+  p.row_tile = tc ? tc_row_tile() : mma ? mma_row_tile(a->dtype, c->D, p.R) : simt_row_tile();
   p.RT = (p.R + p.row_tile - 1) / p.row_tile;
   p.NG = s->B * p.RT;
   const long long cap = (long long)s->max_pages * c->page_size;
-  p.unit_shift = mma ? mma_unit_shift(c->D) : simt_unit_shift();
+  p.unit_shift = tc ? tc_unit_shift() : mma ? mma_unit_shift(c->D) : simt_unit_shift();
   const long long most = std::max(1LL, (long long)p.NG * c->Hkv * ((cap >> p.unit_shift) + 1));
   p.max_ctas = (int)std::min(most, (mma ? mma_ctas_per_sm(c->D, p.row_tile) : 4LL) * device_sm_count());
   p.causal = a->causal ? 1 : 0;
@@ -138,9 +141,14 @@ FwdParams fwd_params(const attn_cache *c, const attn_cache_seqs *s, const attn_c
   p.w_sh = a->weights_stride_h;
   p.Lpad = (cap + 63) / 64 * 64;
   if (mma) p.cluster = mma_cluster(p);
+  if (tc) p.splits = tc_splits(p);
   size_t off = 0;
   L->prefix = L->o_part = L->ml_part = 0;
-  if (!p.cluster) {
+  if (p.splits) {
+    const size_t parts = p.splits > 1 ? (size_t)p.NG * c->Hkv * p.splits : 0;
+    L->o_part = off; off += align_up(parts * p.row_tile * c->D * sizeof(float));
+    L->ml_part = off; off += align_up(parts * p.row_tile * sizeof(float2));
+  } else if (!p.cluster) {
     L->prefix = off; off += align_up(((size_t)p.NG + 1) * sizeof(int));
     L->o_part = off; off += align_up((size_t)2 * p.max_ctas * p.row_tile * c->D * sizeof(float));
     L->ml_part = off; off += align_up((size_t)2 * p.max_ctas * p.row_tile * sizeof(float2));
@@ -204,7 +212,7 @@ size_t attn_cache_fwd_workspace_size(const attn_cache *c, const attn_cache_seqs 
 
 const char *attn_cache_path_name(const attn_cache *c, const attn_cache_seqs *s, const attn_cache_fwd_args *a) {
   if (validate(c, s, a) != ATTN_OK) return "";
-  return use_mma(c) ? "mma" : "simt";
+  return use_tc(c, a) ? "tc" : use_mma(c) ? "mma" : "simt";
 }
 
 int attn_cache_fwd(const attn_cache *c, const attn_cache_seqs *s, const attn_cache_fwd_args *a, void *O,
@@ -224,8 +232,8 @@ int attn_cache_fwd(const attn_cache *c, const attn_cache_seqs *s, const attn_cac
   p.O = O;
   p.LSE = LSE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = use_mma(c) ? launch_fwd_mma(p, a->dtype, c->kind, st) : launch_fwd_simt(p, a->dtype, c->kind, st);
-  if (e == cudaSuccess && !p.cluster) e = launch_fwd_join(p, a->dtype, st);
+  cudaError_t e = p.splits ? launch_fwd_tc(p, c->kind, st) : use_mma(c) ? launch_fwd_mma(p, a->dtype, c->kind, st) : launch_fwd_simt(p, a->dtype, c->kind, st);
+  if (e == cudaSuccess && !p.cluster && p.splits != 1) e = launch_fwd_join(p, a->dtype, st);
   if (e == cudaSuccess && a->weights && s->max_pages > 0) e = launch_weights(p, st);
   return cuda_status(e);
 }

@@ -127,6 +127,7 @@ struct FwdParams {
   int Sq, Hq, G, R;      // R = G * Sq: query rows of one (sequence, kv head); row r is query r / G,
                          // head h * G + r % G
   int row_tile, NG, RT;  // rows per work item; RT = ceil(R / row_tile); NG = B * RT groups (b, tile)
+  int splits;            // shares of every item's keys (tcgen05 path), or 0
   int cluster;           // CTAs of the cluster that has an item (tensor-core path), or 0: items split over the grid
   int unit_shift;        // keys of one unit of work: a slice for each warp of a CTA
   int max_ctas;
@@ -143,8 +144,8 @@ struct FwdParams {
   long long w_sb, w_sh;
   // workspace
   int *prefix;           // [NG + 1]: units of the groups before each; prefix[NG]: units of one kv head
-  float *o_part;         // [2 * max_ctas, row_tile, D]: unnormalised partial outputs
-  float2 *ml_part;       // [2 * max_ctas, row_tile]: exponent reference (base 2) and sum
+  float *o_part;         // [2 * max_ctas or items * splits, row_tile, D]: unnormalised partial outputs
+  float2 *ml_part;       // [the same, row_tile]: exponent reference (base 2) and sum
   float *scores;         // [B * Hkv, R, Lpad]: logits times log2(e), -inf where unseen
   long long Lpad;
 };
@@ -203,6 +204,12 @@ int mma_cluster(const FwdParams &p);
 cudaError_t launch_fwd_mma(const FwdParams &p, int dtype, int kind, cudaStream_t st);
 cudaError_t launch_mma_e4m3(const FwdParams &p, int dtype, cudaStream_t st);
 cudaError_t launch_mma_int8(const FwdParams &p, int dtype, cudaStream_t st);
+// tcgen05 path (many rows).
+bool tc_supported_rows(int dtype, int D, int R);
+int tc_row_tile();
+int tc_unit_shift();
+int tc_splits(const FwdParams &p);
+cudaError_t launch_fwd_tc(const FwdParams &p, int kind, cudaStream_t st);
 bool make_tmap_codes(CUtensorMap *m, const void *base, int D, int page, long long heads, int box_rows);
 
 cudaError_t launch_fwd_join(const FwdParams &p, int dtype, cudaStream_t st);

@@ -250,19 +250,27 @@ __global__ void __launch_bounds__(kThreads) cache_join_kernel(const __grid_const
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = p.c.D;
   const int hk = blockIdx.x / p.NG, g = blockIdx.x - hk * p.NG, b = g / p.RT, rt = g - b * p.RT;
   const int sub = PER_ROW > 1 ? (int)blockIdx.y : (int)blockIdx.y * kWarps + warp, r = rt * p.row_tile + sub;
-  const int first = p.prefix[g], n = p.prefix[g + 1] - first, Uh = p.prefix[p.NG], s = hk * Uh + first;
   if (sub >= p.row_tile || r >= p.R) return;
-  const Shares sh(Uh * p.c.Hkv, p.max_ctas);
-  int c0 = 0, c1 = -1;
-  if (n > 0) {
-    c0 = sh.owner(s);
-    c1 = sh.owner(s + n - 1);
-    if (c0 == c1) return;  // one CTA had the whole item
+  // The parts c0 .. c1 of the item, and where the row's partial of part c lies.
+  int c0 = 0, c1 = -1, second = 0;
+  if (p.splits) {
+    c1 = p.splits - 1;
+  } else {
+    const int first = p.prefix[g], n = p.prefix[g + 1] - first, Uh = p.prefix[p.NG], s = hk * Uh + first;
+    const Shares sh(Uh * p.c.Hkv, p.max_ctas);
+    if (n > 0) {
+      c0 = sh.owner(s);
+      c1 = sh.owner(s + n - 1);
+      if (c0 == c1) return;  // one CTA had the whole item
+      // The item is the second of the first CTA's two if it begins behind that CTA's first unit, and the
+      // first of every later one's.
+      second = s > sh.begin(c0) ? 1 : 0;
+    }
   }
-  // The row's partial of CTA c: the item is the second of the first CTA's two if it begins behind
-  // that CTA's first unit, and the first of every later one's.
-  const int second = n > 0 && s > sh.begin(c0) ? 1 : 0;
-  auto part = [&](int c) { return (size_t)(2 * c + (c == c0 ? second : 0)) * p.row_tile + sub; };
+  auto part = [&](int c) {
+    const size_t slot = p.splits ? (size_t)blockIdx.x * p.splits + c : (size_t)(2 * c + (c == c0 ? second : 0));
+    return slot * p.row_tile + sub;
+  };
   const int me = PER_ROW > 1 ? warp : 0;
   // Running maximum and sum over this warp's parts, four at a time, loads first.
   float M = -CUDART_INF_F, L = 0.f;
@@ -427,7 +435,7 @@ template <typename T> static cudaError_t launch_join_t(const FwdParams &p, cudaS
   const int rows = min(p.row_tile, p.R);
   const unsigned items = (unsigned)(p.NG * p.c.Hkv);
   // Parts per item are at most 1 + CTAs / items on average.
-  if ((long long)items * 4 >= p.max_ctas)
+  if ((long long)items * 4 >= p.max_ctas || (p.splits && p.splits <= 4))
     return launch_dependent(cache_join_kernel<T, 1>, dim3(items, (rows + kWarps - 1) / kWarps), kThreads, 0, st, p);
   return launch_dependent(cache_join_kernel<T, kWarps>, dim3(items, rows), kThreads, 0, st, p);
 }

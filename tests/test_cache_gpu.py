@@ -114,7 +114,8 @@ MASKS = [dict(), dict(causal=True), dict(causal=True, window=1), dict(causal=Tru
 
 
 @pytest.mark.parametrize("kw", MASKS, ids=lambda k: "-".join(f"{a}{b}" for a, b in k.items()) or "all")
-@pytest.mark.parametrize("dtype,D,kind,page", [(BF16, 64, INT8, 32), (BF16, 128, E4M3, 16), (BF16, 256, E4M3, 64), (F32, 48, E4M3, 32)])
+@pytest.mark.parametrize("dtype,D,kind,page", [(BF16, 64, INT8, 32), (BF16, 128, E4M3, 16), (BF16, 256, E4M3, 64), (F32, 48, E4M3, 32), (F32, 256, INT8, 16),
+                                               (F32, 64, E4M3, 64)])
 @pytest.mark.parametrize("Sq", [1, 2, 7, 50])
 def test_masks(kw, dtype, D, kind, page, Sq):
     """Sequences shorter than Sq among them: causal rows that see nothing."""
@@ -147,6 +148,63 @@ def test_long_rows_are_split_and_joined(lengths, Hq, Hkv, D, kind, page, dtype):
     c.check(O, LSE, sink=True, causal=True)
     O2, LSE2 = c.run(causal=True, sink=c.cuda["sink"])
     assert torch.equal(O, O2) and torch.equal(LSE, LSE2)  # the split goes by the lengths alone
+
+
+@pytest.mark.parametrize("kind,D,page", [(E4M3, 128, 64), (INT8, 128, 16), (E4M3, 64, 32), (INT8, 64, 128), (E4M3, 128, 128)])
+@pytest.mark.parametrize("lengths,Sq,Hq,Hkv,kw", [([700, 0, 64, 129, 257], 33, 2, 2, dict(causal=True)), ([5000, 3, 900], 1, 40, 1, {}),
+                                                  ([1000, 1001, 200], 100, 8, 2, dict(causal=True, window=77, softcap=30.0)),
+                                                  ([3000], 300, 4, 1, dict(causal=True)), ([640, 641], 70, 1, 1, dict(softcap=50.0))])
+def test_many_rows(kind, D, page, lengths, Sq, Hq, Hkv, kw):
+    """More than 32 query rows per kv head: the tcgen05 kernel, partial tiles of rows and keys, whole and split."""
+    c = Case(lengths, Sq=Sq, Hq=Hq, Hkv=Hkv, D=D, page=page, kind=kind, seed=Sq + page)
+    t = c.cuda
+    assert fa().attn_cache_path_name(t["q"], c.cache, t["table"], t["lengths"], **kw) == "tc"
+    O, LSE = c.run(sink=t["sink"], **kw)
+    c.check(O, LSE, sink=True, **kw)
+    O2, LSE2 = c.run(sink=t["sink"], **kw)
+    assert torch.equal(O, O2) and torch.equal(LSE, LSE2)
+    assert fa().attn_cache_check_device_status(c.cache) == 0
+
+
+def test_many_rows_with_a_table_far_wider_than_the_lengths():
+    """Shares of keys that some sequences do not have."""
+    c = Case([300, 4000, 0, 65], Sq=40, Hq=4, Hkv=2, page=64, extra_cols=300)
+    w = torch.zeros_like(c.cuda["w"])
+    c.w.zero_()
+    O, LSE = c.run(causal=True, weights=w)
+    c.check(O, LSE, w, causal=True)
+
+
+@pytest.mark.parametrize("kind", [E4M3, INT8])
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_rows_of_bad_pages(kind, D):
+    c = Case([1000, 100], Sq=20, Hq=4, Hkv=2, D=D, page=32, kind=kind)
+    m = fa()
+    hidden = [torch.zeros(1000, dtype=torch.bool), torch.zeros(100, dtype=torch.bool)]
+    bad = c.cuda["table"].clone()
+    for b, col, x in ((0, 1, -1), (0, 13, 2 ** 31 - 1), (0, 31, -5), (1, 0, c.k.shape[0])):
+        bad[b, col] = x
+        hidden[b][col * 32:(col + 1) * 32] = True
+    O, LSE = m.attn_cache_fwd(c.cuda["q"], c.cache, bad, c.cuda["lengths"])
+    assert m.attn_cache_check_device_status(c.cache) == 5
+    c.table = torch.where((bad.cpu() < 0) | (bad.cpu() >= c.k.shape[0]), 0, bad.cpu())
+    c.check(O, LSE, hidden=hidden)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_rows_and_nan_in_the_last_tokens(D):
+    c = Case([400], Sq=24, Hq=8, Hkv=2, D=D)   # queries at 376 .. 399, four heads to a kv head
+    p, slot = int(c.table[0, 390 // 64]), 390 % 64
+    c.v.view(torch.uint8)[p, 0, slot, 3] = 255
+    c.k.view(torch.uint8)[p, 1, slot, 5] = 127
+    c.cuda["v"].copy_(c.v)
+    c.cuda["k"].copy_(c.k)
+    O, LSE = (x.cpu().float() for x in c.run(causal=True))
+    sees = 390 - 376
+    assert torch.isfinite(O[0, :sees]).all() and torch.isfinite(LSE[0, :, :sees]).all()
+    assert torch.isnan(O[0, sees:, :4, 3]).all() and torch.isfinite(LSE[0, :4]).all()
+    assert torch.isfinite(O[0, sees:, :4][..., [x for x in range(D) if x != 3]]).all()
+    assert torch.isnan(O[0, sees:, 4:]).all() and torch.isnan(LSE[0, 4:, sees:]).all()
 
 
 @pytest.mark.parametrize("dtype,D", [(BF16, 64), (BF16, 128), (F32, 64)])
