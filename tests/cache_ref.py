@@ -47,14 +47,16 @@ def gather_scale(s, table_row, n, page):
     return s[table_row[: -(-n // page)].long()].double().repeat_interleave(page, 0)[:n]
 
 
-def attend(q, kv, vv, *, causal=False, window=0, softcap=0.0, sink=None, off_by_one=False, scale=None, hidden=None, vs=None):
+def attend(q, kv, vv, *, causal=False, window=0, softcap=0.0, sink=None, off_by_one=False, scale=None, hidden=None, vs=None, terms=1):
     """One sequence: q [Sq, Hq, D], kv / vv [n, Hkv, D] float64.  Returns O, LSE [Hq, Sq], weights [Hkv, n], and for the
     error bounds sum p |v| [Sq, Hq, D] and the largest sum |q k| * scale.
 
     vs: the values' scales [n, Hkv], for the kernel that rounds its probabilities to fp16.  It rounds p_j vs_j / X with X =
     max_j p_j vs_j (the reference that its exponents subtract is that maximum, or a smaller running one), and multiplies
     v_j / vs_j: where the quotient is below 2^-14, fp16 is subnormal and half a step is 2^-25, not 2^-11 of it.  That adds
-    at most 2^-25 X sum_j |v_j| / vs_j to an output; it is returned with sum p |v|, in units of 2^-11."""
+    at most 2^-25 X sum_j |v_j| / vs_j to an output; it is returned with sum p |v|, in units of 2^-11.
+    terms=2 (float queries): p_j vs_j 2^14 / X is held as the sum of two fp16 numbers; the second is off by half its step, so by
+    2^-22 of the whole, or, where it is subnormal, by 2^-25, that is 2^-39 X.  In units of 2^-20, which bounds() has at least."""
     Sq, Hq, D = q.shape
     n, Hkv, _ = kv.shape
     G = Hq // Hkv
@@ -90,7 +92,7 @@ def attend(q, kv, vv, *, causal=False, window=0, softcap=0.0, sink=None, off_by_
         sx = vs.repeat_interleave(G, 1)                                                    # [n, Hq]
         X = (p * sx.T[:, None, :]).amax(2)                                                 # [Hq, Sq]
         units = (clean.abs() / sx[..., None].clamp(min=2.0 ** -60)).sum(0)                 # [Hq, D]
-        pv = pv + 2.0 ** (-25 + 11) * torch.einsum("hi,hd->ihd", X, units)
+        pv = pv + 2.0 ** (-25 + 11 if terms == 1 else -39 + 20) * torch.einsum("hi,hd->ihd", X, units)
     w = p.sum(1).view(Hkv, G, n).sum(1)
     return o, lse, w, pv, mag
 

@@ -69,8 +69,9 @@ class Case:
             hid = None if hidden is None else hidden[b]
             if hid is not None:
                 kk, vv = torch.where(hid[:, None, None], 0.0, kk), torch.where(hid[:, None, None], 0.0, vv)
-            vs = ref.gather_scale(self.vs, self.table[b], n, self.page) if half else None
-            o, lse, w, pv, mag = ref.attend(self.q[b].double(), kk, vv, sink=self.sink if sink else None, hidden=hid, vs=vs, **kw)
+            vs = ref.gather_scale(self.vs, self.table[b], n, self.page) if self.D in (64, 128, 256) or half else None
+            o, lse, w, pv, mag = ref.attend(self.q[b].double(), kk, vv, sink=self.sink if sink else None, hidden=hid, vs=vs,
+                                            terms=1 if half else 2, **kw)
             e, rel = ref.bounds(self.D, n, mag, kw.get("softcap", 0.0), half)
             store = torch.finfo(self.q.dtype).eps / 2
             lim = store * o.abs() + (1 + store) * rel * pv + 2.0 ** -24 * pv + 1e-37
@@ -410,8 +411,8 @@ def test_codes_past_32_bits():
         kf, vf = (ref.values(c[ids].cpu(), s[ids].cpu()) for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
         row = torch.arange(4)
         kk, vv = ref.gather(kf, row, 450, page), ref.gather(vf, row, 450, page)
-        vs = ref.gather_scale(cache.v_scale[ids].cpu(), row, 450, page) if dtype == BF16 else None
-        o, lse, _, pv, mag = ref.attend(q[0].to(dtype).double(), kk, vv, vs=vs)
+        vs = ref.gather_scale(cache.v_scale[ids].cpu(), row, 450, page)
+        o, lse, _, pv, mag = ref.attend(q[0].to(dtype).double(), kk, vv, vs=vs, terms=1 if dtype == BF16 else 2)
         _, rel = ref.bounds(D, 450, mag, 0.0, dtype == BF16)
         eps = torch.finfo(dtype).eps / 2
         assert ((O[0].cpu().double() - o).abs() <= eps * o.abs() + (1 + eps) * rel * pv).all()
@@ -684,8 +685,9 @@ def test_a_serving_loop(kind, dtype, D, page, window, softcap):
             L = int(n2[b])
             kk, vv = (ref.gather(ref.values(c.cpu(), s.cpu()), table[b].cpu(), L, page)
                       for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
-            vs = ref.gather_scale(cache.v_scale.cpu(), table[b].cpu(), L, page) if dtype == BF16 else None
-            o, lse, ww, pv, mag = ref.attend(q[b].double(), kk, vv, causal=True, window=window, softcap=softcap, sink=sink, vs=vs)
+            vs = ref.gather_scale(cache.v_scale.cpu(), table[b].cpu(), L, page)
+            o, lse, ww, pv, mag = ref.attend(q[b].double(), kk, vv, causal=True, window=window, softcap=softcap, sink=sink, vs=vs,
+                                             terms=1 if dtype == BF16 else 2)
             _, rel = ref.bounds(D, L, mag, softcap, dtype == BF16)
             eps = torch.finfo(dtype).eps / 2
             assert ((O[b].cpu().double() - o).abs() <= eps * o.abs() + (1 + eps) * rel * pv + 1e-37).all()
