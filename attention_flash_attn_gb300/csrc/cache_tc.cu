@@ -351,35 +351,46 @@ cache_tc_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUt
           hide = info[j & 3].gone | info[j & 3].zero;
           partial = hide || pos + kBN > all_below || pos < all_from;
         }
-        constexpr int kPer = D / 16;  // chunks of 16 codes per row
+        constexpr int kPer = D / 16;  // chunks of 16 codes per row, and per thread
+        const int c = t % kPer, row0 = t / kPer, step = 128 / kPer;
+        uint4 u[kPer];
 #pragma unroll
-        for (int y = 0; y < kPer; ++y) {
-          const int c = t % kPer, row = t / kPer + y * (128 / kPer);
-          uint4 *at = reinterpret_cast<uint4 *>(codes + code_at<D>(row, c));
-          uint4 u = *at;
-          if (partial) {  // values only: what no row sees is 0, and so is a NaN, after it is marked
+        for (int y = 0; y < kPer; ++y) u[y] = *reinterpret_cast<const uint4 *>(codes + code_at<D>(row0 + y * step, c));
+        if (partial) {  // values only: what no row sees is 0, and so is a NaN, after it is marked
+#pragma unroll
+          for (int y = 0; y < kPer; ++y) {
+            const int row = row0 + y * step;
             if (pos + row >= key1 || ((hide >> (row >> 4)) & 1u)) {
-              u = make_uint4(0, 0, 0, 0);
+              u[y] = make_uint4(0, 0, 0, 0);
             } else if (KIND == ATTN_CACHE_E4M3) {
-              const uint32_t any = ((u.x & 0x7f7f7f7fu) + 0x01010101u) | ((u.y & 0x7f7f7f7fu) + 0x01010101u) |
-                                   ((u.z & 0x7f7f7f7fu) + 0x01010101u) | ((u.w & 0x7f7f7f7fu) + 0x01010101u);
+              const uint32_t any = ((u[y].x & 0x7f7f7f7fu) + 0x01010101u) | ((u[y].y & 0x7f7f7f7fu) + 0x01010101u) |
+                                   ((u[y].z & 0x7f7f7f7fu) + 0x01010101u) | ((u[y].w & 0x7f7f7f7fu) + 0x01010101u);
               if (any & 0x80808080u) {
-                mark_nans<D>(p, reinterpret_cast<uint8_t *>(at), pos + row, c * 16, range.len, r0, rows, s_nan, misc + 1);
-                u = *at;
+                uint8_t *at = codes + code_at<D>(row, c);
+                mark_nans<D>(p, at, pos + row, c * 16, range.len, r0, rows, s_nan, misc + 1);
+                u[y] = *reinterpret_cast<const uint4 *>(at);
               }
             }
           }
-          uint4 a, d;
-          widen4<KIND>(u.x, a.x, a.y);
-          widen4<KIND>(u.y, a.z, a.w);
-          widen4<KIND>(u.z, d.x, d.y);
-          widen4<KIND>(u.w, d.z, d.w);
-          uint8_t *blk = to + (c / 4) * (kBN * 128);
-          *reinterpret_cast<uint4 *>(blk + sw128(row, 2 * (c % 4))) = a;
-          *reinterpret_cast<uint4 *>(blk + sw128(row, 2 * (c % 4) + 1)) = d;
+          fence_async_smem();  // (codes that mark_nans wrote, before the next load)
         }
-        fence_async_smem();  // for the MMA, and (codes written by mark_nans) for the next load
         mbar_arrive(c_empty(kv));
+        // Chunks 2 (c % 4) and the next of block c / 4; the lanes of the second block store them the other way
+        // round, so that eight lanes meet all banks.
+        uint8_t *const blk = to + (c / 4) * (kBN * 128);
+        const bool swap = (c & 4) != 0;
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) {
+          uint4 a, d;
+          widen4<KIND>(u[y].x, a.x, a.y);
+          widen4<KIND>(u[y].y, a.z, a.w);
+          widen4<KIND>(u[y].z, d.x, d.y);
+          widen4<KIND>(u[y].w, d.z, d.w);
+          const int row = row0 + y * step, ch = 2 * (c % 4) + (swap ? 1 : 0);
+          *reinterpret_cast<uint4 *>(blk + sw128(row, ch)) = swap ? d : a;
+          *reinterpret_cast<uint4 *>(blk + sw128(row, ch ^ 1)) = swap ? a : d;
+        }
+        fence_async_smem();  // for the MMA
         mbar_arrive(kv ? v_full(x) : k_full(x));
       }
     }
