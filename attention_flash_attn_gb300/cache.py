@@ -106,7 +106,7 @@ def attn_cache_fwd(q, cache: AttnCache, table, lengths, *, causal=False, window=
 
 def attn_cache_path_name(q, cache: AttnCache, table, lengths, *, causal=False, window=0, softcap=0.0, sink=None,
                          off_by_one=False, scale=None, weights=None, weights_out=None) -> str:
-    """Kernel path attn_cache_fwd takes for these arguments: "mma" (tensor cores) or "simt"."""
+    """Kernel path attn_cache_fwd takes for these arguments: "tc" (tcgen05), "mma" (warp-level tensor-core products) or "simt"."""
     return _calls().path(cache._addr, cache.k, q, table, lengths, causal, window, softcap, sink, off_by_one, scale, weights,
                          weights_out)
 

@@ -1,8 +1,8 @@
 // cache_tc.cu -- attention over the 8-bit cache with tcgen05: bf16 queries, head dims 64 and 128, many query
 // rows per kv head (drafts of several tokens, chunks of a prompt, many heads to a kv head).
 //
-// m16n8k16 products end at some 330 TFLOP/s here, which is 24 rows at the memory's rate; from there on the
-// tensor cores' own path is needed.  One CTA computes one 128-row tile of one (sequence, kv head) over one
+// m16n8k16 products end at some 330 TFLOP/s here; with many rows the tensor cores' own path does more (570 TFLOP/s
+// for 2048 rows of 16111 keys at D = 128).  One CTA computes one 128-row tile of one (sequence, kv head) over one
 // share of its keys, in tiles of 128 keys:
 //   warp 0        TMA: the tile's codes of K and V, page by page, and the scales of its 16-key groups into a
 //                 small ring;
@@ -12,8 +12,11 @@
 //   warps 10..13  converters: the queries once, scaled per row by a power of two into fp16, then every tile's
 //                 codes widened to fp16 (exactly) into the 128-byte-swizzled operand layout.
 // Scales never touch the operands: a key's scale multiplies its scores, a value's enters the exponent of the
-// probabilities, as in the kernel for few rows (cache_work.cuh).  Bound by the exponentials (one per score:
-// 128 x 128 at 16 a clock) and the two MMAs (some 544 clocks each) per tile, which overlap.
+// probabilities, as in the kernel for few rows (cache_work.cuh).  What bounds it now, of some
+// 3500 clocks a tile: the softmax warps are busy for 2900 of them (the exponentials alone, 128 x 128 at 16 a
+// clock, take 1024) and the converters for 2700; the two MMAs take 544 each.  Twice the converter warps, with
+// registers moved to the softmax (640 threads), and converters for K and V apart were slower (258 and 270 us
+// against 233): shared memory is what they share.
 #include <algorithm>
 
 #include "cache_work.cuh"
@@ -381,14 +384,15 @@ cache_tc_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUt
         const bool swap = (c & 4) != 0;
 #pragma unroll
         for (int y = 0; y < kPer; ++y) {
+          const uint32_t w0 = swap ? u[y].z : u[y].x, w1 = swap ? u[y].w : u[y].y, w2 = swap ? u[y].x : u[y].z, w3 = swap ? u[y].y : u[y].w;
           uint4 a, d;
-          widen4<KIND>(u[y].x, a.x, a.y);
-          widen4<KIND>(u[y].y, a.z, a.w);
-          widen4<KIND>(u[y].z, d.x, d.y);
-          widen4<KIND>(u[y].w, d.z, d.w);
+          widen4<KIND>(w0, a.x, a.y);
+          widen4<KIND>(w1, a.z, a.w);
+          widen4<KIND>(w2, d.x, d.y);
+          widen4<KIND>(w3, d.z, d.w);
           const int row = row0 + y * step, ch = 2 * (c % 4) + (swap ? 1 : 0);
-          *reinterpret_cast<uint4 *>(blk + sw128(row, ch)) = swap ? d : a;
-          *reinterpret_cast<uint4 *>(blk + sw128(row, ch ^ 1)) = swap ? a : d;
+          *reinterpret_cast<uint4 *>(blk + sw128(row, ch)) = a;
+          *reinterpret_cast<uint4 *>(blk + sw128(row, ch ^ 1)) = d;
         }
         fence_async_smem();  // for the MMA
         mbar_arrive(kv ? v_full(x) : k_full(x));
@@ -492,22 +496,25 @@ cache_tc_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUt
         m_ref = m_new;
       }
       const float mr = m_ref == -CUDART_INF_F ? 0.f : m_ref;
-      uint32_t pk[kHC / 2];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const float ref = lv[g] - mr;
-        float sum = 0.f;
+      for (int q = 0; q < 2; ++q) {  // (16 registers of P at a time)
+        uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float p0 = ex2_approx(fmaf(f[g], __uint_as_float(xr[16 * g + 2 * e]), ref));
-          const float p1 = ex2_approx(fmaf(f[g], __uint_as_float(xr[16 * g + 2 * e + 1]), ref));
-          sum += p0 + p1;
-          pk[8 * g + e] = pack_h2(p0, p1);
+        for (int g = 2 * q; g < 2 * q + 2; ++g) {
+          const float ref = lv[g] - mr;
+          float sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float p0 = ex2_approx(fmaf(f[g], __uint_as_float(xr[16 * g + 2 * e]), ref));
+            const float p1 = ex2_approx(fmaf(f[g], __uint_as_float(xr[16 * g + 2 * e + 1]), ref));
+            sum += p0 + p1;
+            pk[8 * (g - 2 * q) + e] = pack_h2(p0, p1);
+          }
+          l = fmaf(sum, ex2_approx(-lv[g]), l);
         }
-        l = fmaf(sum, ex2_approx(-lv[g]), l);
+        __syncwarp();
+        tmem_st16(sa + 16 * q, pk);
       }
-      __syncwarp();
-      tmem_st32(sa, *reinterpret_cast<const uint32_t(*)[32]>(pk));
       if (j >= 1) ok = mbar_wait_warp(o_done, (j - 1) & 1, p.c.status);
       if (j >= 1 && __any_sync(~0u, alpha != 1.f)) {
         tc_fence_after();
@@ -611,8 +618,11 @@ template <int KIND, int D> cudaError_t launch_t(const FwdParams &p, cudaStream_t
 int tc_row_tile() { return kBM; }
 int tc_unit_shift() { return 7; }
 
-// From how many rows per kv head this kernel is taken.
-bool tc_supported_rows(int dtype, int D, int R) { return dtype == kBF16 && (D == 64 || D == 128) && R > 32; }
+// From how many rows per kv head this kernel is taken.  Measured against the kernel of cache_mma.cuh (us, this /
+// that), D = 128 with 8 kv heads: 16 ragged rows up to 8192 keys, 36 query rows 128 / 98, 64 131 / 109, 96
+// 136 / 159, 128 141 / 209; one row of 16111 keys, 96 rows 37 / 41, 2048 rows 234 / 430.  D = 64, where a tile's
+// MMAs are half and its softmax is not: 160 rows 49 / 37, 512 78 / 72, 1024 125 / 129, 2048 193 / 244.
+bool tc_supported_rows(int dtype, int D, int R) { return dtype == kBF16 && ((D == 128 && R > 64) || (D == 64 && R > 512)); }
 
 // Shares of an item's keys, one CTA each, one CTA per SM: enough for three waves (the block scheduler then
 // evens ragged rows out), of at least four tiles.

@@ -152,12 +152,13 @@ def test_long_rows_are_split_and_joined(lengths, Hq, Hkv, D, kind, page, dtype):
 
 
 @pytest.mark.parametrize("kind,D,page", [(E4M3, 128, 64), (INT8, 128, 16), (E4M3, 64, 32), (INT8, 64, 128), (E4M3, 128, 128)])
-@pytest.mark.parametrize("lengths,Sq,Hq,Hkv,kw", [([700, 0, 64, 129, 257], 33, 2, 2, dict(causal=True)), ([5000, 3, 900], 1, 40, 1, {}),
-                                                  ([1000, 1001, 200], 100, 8, 2, dict(causal=True, window=77, softcap=30.0)),
-                                                  ([3000], 300, 4, 1, dict(causal=True)), ([640, 641], 70, 1, 1, dict(softcap=50.0))])
-def test_many_rows(kind, D, page, lengths, Sq, Hq, Hkv, kw):
-    """More than 32 query rows per kv head: the tcgen05 kernel, partial tiles of rows and keys, whole and split."""
-    c = Case(lengths, Sq=Sq, Hq=Hq, Hkv=Hkv, D=D, page=page, kind=kind, seed=Sq + page)
+@pytest.mark.parametrize("lengths,Sq,G,Hkv,kw", [([700, 0, 64, 129, 257], 33, 2, 2, dict(causal=True)), ([5000, 3, 900], 1, 80, 1, {}),
+                                                 ([1000, 1001, 200], 100, 4, 2, dict(causal=True, window=77, softcap=30.0)),
+                                                 ([3000], 300, 4, 1, dict(causal=True)), ([640, 641], 70, 1, 1, dict(softcap=50.0))])
+def test_many_rows(kind, D, page, lengths, Sq, G, Hkv, kw):
+    """More than 64 (head dim 64: 512) query rows per kv head: the tcgen05 kernel, partial tiles of rows and keys, whole and split."""
+    G = G if D == 128 else 8 * G
+    c = Case(lengths, Sq=Sq, Hq=G * Hkv, Hkv=Hkv, D=D, page=page, kind=kind, seed=Sq + page)
     t = c.cuda
     assert fa().attn_cache_path_name(t["q"], c.cache, t["table"], t["lengths"], **kw) == "tc"
     O, LSE = c.run(sink=t["sink"], **kw)
@@ -179,7 +180,7 @@ def test_many_rows_with_a_table_far_wider_than_the_lengths():
 @pytest.mark.parametrize("kind", [E4M3, INT8])
 @pytest.mark.parametrize("D", [64, 128])
 def test_many_rows_of_bad_pages(kind, D):
-    c = Case([1000, 100], Sq=20, Hq=4, Hkv=2, D=D, page=32, kind=kind)
+    c = Case([1000, 100], Sq=40, Hq=4 if D == 128 else 32, Hkv=2, D=D, page=32, kind=kind)
     m = fa()
     hidden = [torch.zeros(1000, dtype=torch.bool), torch.zeros(100, dtype=torch.bool)]
     bad = c.cuda["table"].clone()
@@ -194,18 +195,20 @@ def test_many_rows_of_bad_pages(kind, D):
 
 @pytest.mark.parametrize("D", [64, 128])
 def test_many_rows_and_nan_in_the_last_tokens(D):
-    c = Case([400], Sq=24, Hq=8, Hkv=2, D=D)   # queries at 376 .. 399, four heads to a kv head
+    G = 4 if D == 128 else 32
+    c = Case([400], Sq=24, Hq=2 * G, Hkv=2, D=D)   # queries at 376 .. 399
     p, slot = int(c.table[0, 390 // 64]), 390 % 64
     c.v.view(torch.uint8)[p, 0, slot, 3] = 255
     c.k.view(torch.uint8)[p, 1, slot, 5] = 127
     c.cuda["v"].copy_(c.v)
     c.cuda["k"].copy_(c.k)
+    assert fa().attn_cache_path_name(c.cuda["q"], c.cache, c.cuda["table"], c.cuda["lengths"]) == "tc"
     O, LSE = (x.cpu().float() for x in c.run(causal=True))
     sees = 390 - 376
     assert torch.isfinite(O[0, :sees]).all() and torch.isfinite(LSE[0, :, :sees]).all()
-    assert torch.isnan(O[0, sees:, :4, 3]).all() and torch.isfinite(LSE[0, :4]).all()
-    assert torch.isfinite(O[0, sees:, :4][..., [x for x in range(D) if x != 3]]).all()
-    assert torch.isnan(O[0, sees:, 4:]).all() and torch.isnan(LSE[0, 4:, sees:]).all()
+    assert torch.isnan(O[0, sees:, :G, 3]).all() and torch.isfinite(LSE[0, :G]).all()
+    assert torch.isfinite(O[0, sees:, :G][..., [x for x in range(D) if x != 3]]).all()
+    assert torch.isnan(O[0, sees:, G:]).all() and torch.isnan(LSE[0, G:, sees:]).all()
 
 
 @pytest.mark.parametrize("dtype,D", [(BF16, 64), (BF16, 128), (F32, 64)])
