@@ -45,7 +45,7 @@ int validate(const attn_cache *c, const attn_cache_seqs *s) {
   if (!s->lengths || !aligned4(s->lengths)) return ATTN_ERR_INVALID;
   if (s->max_pages > 0 && (!s->table || !aligned4(s->table))) return ATTN_ERR_INVALID;
   if (s->table_stride < (s->B > 1 ? s->max_pages : 0)) return ATTN_ERR_INVALID;
-  if ((long long)s->B * c->Hkv > INT_MAX / 8) return ATTN_ERR_UNSUPPORTED;  // grids (clusters of 8)
+  if ((long long)s->B * c->Hkv > INT_MAX / 16) return ATTN_ERR_UNSUPPORTED;  // grids (clusters of up to 16)
   return ATTN_OK;
 }
 

@@ -2,8 +2,8 @@
 //
 // The new rows' largest magnitude gives the scale they need, the least power of two; a page that holds
 // earlier tokens keeps the larger of that and its present scale, and when it grows, the earlier codes are
-// moved to it.  Prompts: one block per (sequence, page the new tokens touch, kv head, K or V), which
-// reads its rows once, into registers (what does not fit there it reads again, from L2).  Single tokens: one warp each.  Bound by reading the new rows (2 or
+// moved to it.  Prompts: one block per (sequence, page the new tokens touch, kv head), which
+// reads its rows of K and V once, into registers (what does not fit there it reads again, from L2).  Single tokens: one warp each.  Bound by reading the new rows (2 or
 // 4 bytes a value) and writing codes (1 byte); a step of single tokens by the chain length -> page ->
 // scale.
 #include "cache_common.cuh"
@@ -79,16 +79,18 @@ __device__ __forceinline__ float warp_max(float x) {
   for (int o = 16; o; o >>= 1) x = max_nan(x, __shfl_xor_sync(~0u, x, o));
   return x;
 }
-// Maximum over the block; every thread gets it.
-__device__ __forceinline__ float block_max(float x) {
-  __shared__ float s_m[kThr / 32];
-  x = warp_max(x);
+// Two maxima over the block; every thread gets them.
+__device__ __forceinline__ void block_max2(float *x) {
+  __shared__ float2 s_m[kThr / 32];
+  const float a = warp_max(x[0]), b = warp_max(x[1]);
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) s_m[threadIdx.x >> 5] = x;
+  if ((threadIdx.x & 31) == 0) s_m[threadIdx.x >> 5] = make_float2(a, b);
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kThr / 32; ++w) x = max_nan(x, s_m[w]);
-  return x;
+  for (int w = 0; w < kThr / 32; ++w) {
+    x[0] = max_nan(x[0], s_m[w].x);
+    x[1] = max_nan(x[1], s_m[w].y);
+  }
 }
 
 // Where a sequence's new tokens go: positions [len, end).  Writes the new length and records what is
@@ -140,94 +142,110 @@ template <typename T, int KIND>
 __global__ void __launch_bounds__(kThr) cache_append_kernel(const __grid_constant__ AppendParams p) {
   const View &c = p.c;
   const int b = blockIdx.x / p.span, nth = blockIdx.x - b * p.span, h = blockIdx.y, t = threadIdx.x;
-  const bool val = blockIdx.z == 1;
-  const Span sp = new_span(p, b, nth == 0 && h == 0 && !val && t == 0);
+  const Span sp = new_span(p, b, nth == 0 && h == 0 && t == 0);
   const int len = sp.len, col = (len >> c.page_shift) + nth;  // column of the table
   const int first = max(len, col << c.page_shift);            // the page's new positions: [first, last)
   const int last = min((long long)sp.end, ((long long)col + 1) << c.page_shift);
   if (first >= last) return;
   const int D = c.D, per = D / 8, total = (last - first) * per, old = first & (c.page - 1);
-  const long long ss = val ? p.v_ss : p.k_ss;
-  const T *src = static_cast<const T *>(val ? p.v : p.k) + b * (val ? p.v_sb : p.k_sb) + h * (val ? p.v_sh : p.k_sh) + (first - len) * ss;
-  // This thread's pieces: t, t + kThr, ... of the rows' pieces in order.
-  const int row0 = t / per, dr = kThr / per, dp = kThr - dr * per;
-  int piece = t - row0 * per;
-  const T *at = src + row0 * ss + piece * 8;
+  const T *src[2] = {static_cast<const T *>(p.k) + b * p.k_sb + h * p.k_sh + (first - len) * p.k_ss,
+                     static_cast<const T *>(p.v) + b * p.v_sb + h * p.v_sh + (first - len) * p.v_ss};
+  const long long ss[2] = {p.k_ss, p.v_ss};
+  // This thread's pieces of the rows, in order: t, t + kThr, ...; row and place in the row of the current one.
+  const int row0 = t / per, piece0 = t - row0 * per, dr = kThr / per, dp = kThr - dr * per;
+  int row = row0, piece = piece0;
   auto advance = [&]() {
+    row += dr;
     piece += dp;
-    at += dr * ss + dp * 8;
     if (piece >= per) {
       piece -= per;
-      at += ss - per * 8;
+      ++row;
     }
   };
-  Raw<T> held[kHeld];
+  auto fetch = [&](int kv, Raw<T> &v) { v.load(src[kv] + row * ss[kv] + piece * 8); };
+  Raw<T> held[2][kHeld];
 #pragma unroll
   for (int x = 0; x < kHeld; ++x) {
-    held[x].zero();
-    if (t + x * kThr < total) held[x].load(at);
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      held[kv][x].zero();
+      if (t + x * kThr < total) fetch(kv, held[kv][x]);
+    }
     advance();
   }
-  const T *const rest = at;
-  const int rest_piece = piece;
+  const int rest_row = row, rest_piece = piece;
   const int page = page_of(c, b, first);
-  if (!val && p.weights)
+  if (p.weights)
     for (int x = first + t; x < last; x += kThr) p.weights[b * p.w_sb + h * p.w_sh + x] = 0.f;
   if (page < 0) return;
-  uint8_t *dst = (val ? c.v : c.k) + row_at(c, page, h, 0);
-  float *sc = (val ? c.v_scale : c.k_scale) + (size_t)page * c.Hkv + h;
-  const float was = *sc;
-  float amax = 0.f;
+  const size_t sc = (size_t)page * c.Hkv + h, at = row_at(c, page, h, 0);
+  const float was[2] = {c.k_scale[sc], c.v_scale[sc]};
+  float amax[2] = {0.f, 0.f};
 #pragma unroll
-  for (int x = 0; x < kHeld; ++x) amax = max_nan(amax, held[x].amax());
+  for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll
+    for (int x = 0; x < kHeld; ++x) amax[kv] = max_nan(amax[kv], held[kv][x].amax());
+    row = rest_row;
+    piece = rest_piece;
 #pragma unroll 1
-  for (int i = t + kHeld * kThr; i < total; i += kThr) {  // pages of more than 8192 values
-    Raw<T> v;
-    v.load(at);
-    advance();
-    amax = max_nan(amax, v.amax());
-  }
-  amax = block_max(amax);  // (and every thread has read the old scale)
-  const bool fit = amax <= kMaxFloat;
-  if (!fit) {  // something is infinite or NaN: the scale goes by the rest
-    if (t == 0) set_status(c.status, kStatusNonFinite);
-    amax = 0.f;
-    at = src + row0 * ss + (t - row0 * per) * 8;
-    piece = t - row0 * per;
-#pragma unroll 1
-    for (int i = t; i < total; i += kThr) {
+    for (int i = t + kHeld * kThr; i < total; i += kThr) {  // pages of more than 8192 values
       Raw<T> v;
-      v.load(at);
+      fetch(kv, v);
       advance();
-      float x[8];
-      v.get(x);
-      amax = amax_finite(x, amax);
+      amax[kv] = max_nan(amax[kv], v.amax());
     }
-    amax = block_max(amax);
   }
-  float s = need_scale<KIND>(amax);
-  if (old > 0 && was >= s) s = was;
-  const float inv = 1.f / s;  // exact for the powers of two that this library writes
-  uint2 *to = reinterpret_cast<uint2 *>(dst + (size_t)old * D);
-  auto put = [&](int i, const Raw<T> &v) {
-    float x[8];
-    v.get(x);
-    to[i] = fit ? encode8<KIND, true>(x, inv) : encode8<KIND, false>(x, inv);
-  };
+  block_max2(amax);  // (and every thread has read the old scales)
 #pragma unroll
-  for (int x = 0; x < kHeld; ++x)
-    if (t + x * kThr < total) put(t + x * kThr, held[x]);
-  at = rest;
-  piece = rest_piece;
+  for (int kv = 0; kv < 2; ++kv) {
+    const bool fit = amax[kv] <= kMaxFloat;
+    if (!fit) {  // something is infinite or NaN: the scale goes by the rest
+      if (t == 0) set_status(c.status, kStatusNonFinite);
+      float m[2] = {0.f, 0.f};
+      row = row0;
+      piece = piece0;
 #pragma unroll 1
-  for (int i = t + kHeld * kThr; i < total; i += kThr) {
-    Raw<T> v;
-    v.load(at);
-    advance();
-    put(i, v);
+      for (int i = t; i < total; i += kThr) {
+        Raw<T> v;
+        fetch(kv, v);
+        advance();
+        float x[8];
+        v.get(x);
+        m[0] = amax_finite(x, m[0]);
+      }
+      block_max2(m);
+      amax[kv] = m[0];
+    }
+    float s = need_scale<KIND>(amax[kv]);
+    if (old > 0 && was[kv] >= s) s = was[kv];
+    const float inv = 1.f / s;  // exact for the powers of two that this library writes
+    uint8_t *dst = (kv ? c.v : c.k) + at;
+    uint2 *to = reinterpret_cast<uint2 *>(dst + (size_t)old * D);
+    if (fit) {
+#pragma unroll
+      for (int x = 0; x < kHeld; ++x)
+        if (t + x * kThr < total) {
+          float v[8];
+          held[kv][x].get(v);
+          to[t + x * kThr] = encode8<KIND, true>(v, inv);
+        }
+    }
+    if (!fit || total > kHeld * kThr) {
+      row = fit ? rest_row : row0;
+      piece = fit ? rest_piece : piece0;
+#pragma unroll 1
+      for (int i = t + (fit ? kHeld * kThr : 0); i < total; i += kThr) {
+        Raw<T> v;
+        fetch(kv, v);
+        advance();
+        float x[8];
+        v.get(x);
+        to[i] = encode8<KIND, false>(x, inv);
+      }
+    }
+    if (old > 0 && s != was[kv]) rescale<KIND>(reinterpret_cast<uint4 *>(dst), old * (D / 16), was[kv] * inv, t, kThr);
+    if (t == 0) (kv ? c.v_scale : c.k_scale)[sc] = s;
   }
-  if (old > 0 && s != was) rescale<KIND>(reinterpret_cast<uint4 *>(dst), old * (D / 16), was * inv, t, kThr);
-  if (t == 0) *sc = s;
 }
 
 // S = 1: warp w of the grid has (sequence, kv head, K or V).  The row is fetched before the chain that
@@ -280,7 +298,7 @@ template <typename T, int KIND> cudaError_t launch_append_t(const AppendParams &
     const long long tasks = 2LL * p.c.B * p.c.Hkv;
     cache_append_token_kernel<T, KIND><<<(unsigned)((tasks + 3) / 4), 128, 0, st>>>(p);
   } else {
-    cache_append_kernel<T, KIND><<<dim3((unsigned)(p.c.B * p.span), (unsigned)p.c.Hkv, 2), kThr, 0, st>>>(p);
+    cache_append_kernel<T, KIND><<<dim3((unsigned)(p.c.B * p.span), (unsigned)p.c.Hkv), kThr, 0, st>>>(p);
   }
   return counted(cudaGetLastError());
 }
