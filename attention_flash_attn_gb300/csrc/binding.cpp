@@ -92,6 +92,9 @@ void same_device(const char *where, const Cache &c, const at::Tensor &t) {
     raise(PyExc_ValueError, "%s: every tensor must be on %s (got one on %s)", where, c.device().str().c_str(), t.device().str().c_str());
 }
 
+// Stride of a dimension, 0 where it is never taken (PyTorch leaves any number there).
+int64_t stride(const at::Tensor &t, int d) { return t.size(d) > 1 ? t.stride(d) : 0; }
+
 // [B, S, H, D] rows in bfloat16 or float32 with the head dimension dense; returns the dtype code.
 int rows(const char *where, const char *name, const at::Tensor &t, const Cache &c) {
   const auto ty = t.scalar_type();
@@ -198,8 +201,8 @@ PyObject *append(PyObject *const *a, Py_ssize_t n) {
   g.S = (int)k.size(1);
   g.k = k.data_ptr();
   g.v = v.data_ptr();
-  g.k_stride_b = k.stride(0); g.k_stride_s = k.stride(1); g.k_stride_h = k.stride(2);
-  g.v_stride_b = v.stride(0); g.v_stride_s = v.stride(1); g.v_stride_h = v.stride(2);
+  g.k_stride_b = stride(k, 0); g.k_stride_s = stride(k, 1); g.k_stride_h = stride(k, 2);
+  g.v_stride_b = stride(v, 0); g.v_stride_s = stride(v, 1); g.v_stride_h = stride(v, 2);
   if (a[6] != Py_None) {
     const at::Tensor &t = tensor(where, "counts", a[6]);
     ints(where, "counts", t, B, c);
@@ -229,7 +232,7 @@ void fwd_args(const char *where, const Cache &c, PyObject *const *a, attn_cache_
   g->Sq = (int)q.size(1);
   g->Hq = (int)Hq;
   g->q = q.data_ptr();
-  g->q_stride_b = q.stride(0); g->q_stride_s = q.stride(1); g->q_stride_h = q.stride(2);
+  g->q_stride_b = stride(q, 0); g->q_stride_s = stride(q, 1); g->q_stride_h = stride(q, 2);
   g->causal = truth(a[5]);
   g->window = whole32(where, "window", a[6]);
   g->softcap = (float)real(a[7]);

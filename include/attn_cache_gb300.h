@@ -15,8 +15,8 @@
  * Scales written by this library are powers of two,
  *   need(amax) = the least 2^e >= 2^-60 with amax <= qmax * 2^e    (qmax: 448 e4m3, 127 int8),
  * so that dividing by them is exact, and moving e4m3 codes to a larger scale is exact but for
- * codes that become subnormal.  Attention takes any finite scale; a value scale below 2^-60
- * counts as 0.
+ * codes that become subnormal.  Attention and eviction take any scale, up to 2^100 for values; a
+ * value scale below 2^-60 counts as 0.
  *
  * Errors found on the device (a page id outside [0, num_pages) at a position below the length, a
  * length below 0 or past the table) are recorded in the cache's status word, read and cleared

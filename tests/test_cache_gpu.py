@@ -277,6 +277,18 @@ def test_scales_that_differ_by_powers(dtype, D):
     assert (O == 0).all()
 
 
+@pytest.mark.parametrize("dtype,D,Hq", [(BF16, 64, 8), (BF16, 128, 8), (BF16, 128, 160), (BF16, 256, 8), (F32, 128, 8), (F32, 48, 8)])
+@pytest.mark.parametrize("kind", [E4M3, INT8])
+def test_scales_that_are_no_powers_of_two(dtype, D, Hq, kind):
+    """As another writer may have left them."""
+    c = Case([500, 70], Hq=Hq, Hkv=2, D=D, kind=kind, dtype=dtype)
+    g = torch.Generator().manual_seed(3)
+    for s, name in ((c.ks, "ks"), (c.vs, "vs")):
+        s *= torch.rand(s.shape, generator=g) + 0.5
+        c.cuda[name].copy_(s)
+    c.check(*c.run())
+
+
 @pytest.mark.parametrize("std", [1e-20, 1e-6, 300.0])
 def test_magnitudes_of_queries(std):
     """Far from 1, where fp16 alone would overflow or vanish; the scale brings the logits back."""
@@ -550,6 +562,44 @@ def test_append_into_bad_pages_and_past_the_table():
     assert (cache2.k.float() == 0).all()
 
 
+def test_append_counts_outside_their_range_and_strides_of_single_rows():
+    m = fa()
+    cache = m.AttnCache.empty(8, 16, 2, 32)
+    table = torch.arange(8, dtype=torch.int32).view(4, 2).cuda()
+    big = torch.ones((4, 2, 35), device="cuda")
+    x = torch.as_strided(big, (4, 3, 2, 32), (64, 0, 32, 1), 0)    # three equal rows
+    n = m.attn_cache_append(cache, x, x, table, torch.zeros(4, dtype=torch.int32, device="cuda"), counts=i32(-3, 0, 2, 99).cuda())
+    assert n.tolist() == [0, 0, 2, 3] and m.attn_cache_check_device_status(cache) == 0
+    assert (cache.k.float()[0:4] == 0).all() and (cache.k.float()[6, :, :3] * cache.k_scale[6, :, None, None] == 1).all()
+    one = torch.as_strided(big, (1, 1, 2, 32), (5, 3, 64, 1), 0)   # odd strides where nothing steps
+    assert m.attn_cache_append(cache, one, one, table[:1], i32(7).cuda()).tolist() == [8]
+    q = torch.as_strided(big, (1, 1, 2, 32), (7, 1, 32, 1), 0)
+    O, _ = m.attn_cache_fwd(q, cache, table[2:3], i32(2).cuda())
+    assert torch.equal(O, torch.ones_like(O))
+
+
+def test_append_on_a_scale_that_is_no_power_of_two():
+    m = fa()
+    for kind in (E4M3, INT8):
+        k, v, ks, vs = ref.make_cache(3, 2, 32, 64, kind, std=4.0)
+        ks *= 1.37
+        vs *= 0.77
+        cache = m.AttnCache(k.cuda(), v.cuda(), ks.cuda(), vs.cuda())
+        table = i32(1, 2).cuda()[None]
+        x = torch.randn((1, 5, 2, 64), generator=torch.Generator().manual_seed(1)) * 0.1
+        m.attn_cache_append(cache, x.cuda(), 500 * x.cuda(), table, i32(20).cuda())
+        assert torch.equal(cache.k_scale.cpu(), ks)                    # the present scale holds the new rows
+        got = ref.values(cache.k.cpu(), cache.k_scale.cpu())[1, :, 20:25].transpose(0, 1)
+        s = ks[1].double()[None, :, None]
+        step = s if kind == INT8 else torch.maximum(2.0 ** -9 * s, 2.0 ** -3 * x[0].double().abs())
+        assert ((got - x[0].double()).abs() <= 0.5 * step * (1 + 2.0 ** -20)).all()
+        assert ((cache.v_scale[1].cpu().log2() % 1) == 0).all()         # the other had to grow, to a power of two
+        old = ref.values(v, vs)[1, :, :20]
+        now = ref.values(cache.v.cpu(), cache.v_scale.cpu())[1, :, :20]
+        s = cache.v_scale[1].cpu().double()[:, None, None]
+        assert ((now - old).abs() <= 0.5 * (1 + 2.0 ** -20) * (s if kind == INT8 else torch.maximum(2.0 ** -9 * s, 2.0 ** -3 * old.abs()))).all()
+
+
 def test_append_no_rows():
     m = fa()
     cache = m.AttnCache.empty(2, 16, 1, 16)
@@ -561,9 +611,11 @@ def test_append_no_rows():
 
 # ---------------------------------------------------------------- eviction
 
-def evict_case(lengths, *, keep, recent=0, first=0, H=2, page=64, D=64, kind=E4M3, seed=0, weights=None):
+def evict_case(lengths, *, keep, recent=0, first=0, H=2, page=64, D=64, kind=E4M3, seed=0, weights=None, scales=None):
     m = fa()
     c = Case(lengths, Hq=H, Hkv=H, D=D, page=page, kind=kind, seed=seed)
+    if scales is not None:
+        c.ks, c.vs = scales(c.ks), scales(c.vs)
     B = len(lengths)
     g = torch.Generator().manual_seed(seed)
     w = torch.randn(c.w.shape, generator=g).exp() if weights is None else weights(c.w.shape, g)
@@ -622,6 +674,14 @@ def test_evict_ties_and_special_weights():
     for f in (ties, special):
         for keep, recent, first in ((50, 0, 0), (333, 20, 7), (90, 89, 0)):
             evict_case([600, 340, 334], keep=keep, recent=recent, first=first, weights=f)
+
+
+@pytest.mark.parametrize("kind", [E4M3, INT8])
+def test_evict_scales_that_are_no_powers_of_two_or_far_apart(kind):
+    g = torch.Generator().manual_seed(8)
+    evict_case([400, 130], keep=90, recent=10, kind=kind, scales=lambda s: s * (torch.rand(s.shape, generator=g) + 0.5))
+    evict_case([400, 130], keep=90, recent=10, kind=kind, scales=lambda s: s * torch.exp2(torch.randint(-30, 30, s.shape, generator=g).float()))
+    evict_case([400, 130], keep=90, recent=10, kind=kind, scales=lambda s: s * 0.0)
 
 
 @pytest.mark.parametrize("n,keep", [(70001, 4096), (131072, 1000), (40000, 39999), (33000, 2)])
