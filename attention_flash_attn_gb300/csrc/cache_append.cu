@@ -2,10 +2,12 @@
 //
 // The new rows' largest magnitude gives the scale they need, the least power of two; a page that holds
 // earlier tokens keeps the larger of that and its present scale, and when it grows, the earlier codes are
-// moved to it.  Prompts: one block per (sequence, page the new tokens touch, kv head), which
-// reads its rows of K and V once, into registers (what does not fit there it reads again, from L2).  Single tokens: one warp each.  Bound by reading the new rows (2 or
-// 4 bytes a value) and writing codes (1 byte); a step of single tokens by the chain length -> page ->
-// scale.
+// moved to it.  Prompts: one block per (sequence, page the new tokens touch, kv head), which reads its rows
+// of K and V once, into registers (what does not fit there it reads again, from L2): 27 us for 8 ragged
+// prompts of up to 4096 tokens, 8 heads, D = 128, bf16, 132 MB at 4.9 TB/s.  One block for K and one for V
+// each took 31.  Single tokens: one warp each, 4 us for 4 sequences, 5 for 192.  Prompts are bound by reading
+// the new rows (2 or 4 bytes a value) and writing codes (1 byte); single tokens by the chain length -> page
+// -> scale, three loads that wait for one another, and by the launch.
 #include "cache_common.cuh"
 
 namespace attn {

@@ -197,6 +197,7 @@ int simt_unit_shift();
 
 // Tensor-core path.
 bool mma_supported(int D);
+int mma_columns(int D);
 int mma_row_tile(int dtype, int D, int R);
 int mma_ctas_per_sm(int D, int row_tile);
 int mma_unit_shift(int D);
@@ -210,7 +211,7 @@ int tc_row_tile();
 int tc_unit_shift();
 int tc_splits(const FwdParams &p);
 cudaError_t launch_fwd_tc(const FwdParams &p, int kind, cudaStream_t st);
-bool make_tmap_codes(CUtensorMap *m, const void *base, int D, int page, long long heads, int box_rows);
+bool make_tmap_codes(CUtensorMap *m, const void *base, int D, int page, long long heads, int box_cols, int box_rows);
 
 cudaError_t launch_fwd_join(const FwdParams &p, int dtype, cudaStream_t st);
 cudaError_t launch_weights(const FwdParams &p, cudaStream_t st);

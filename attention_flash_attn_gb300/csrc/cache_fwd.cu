@@ -1,6 +1,5 @@
-// cache_fwd.cu -- attention over the 8-bit cache on fp32 FFMA (fp32 queries, head dims without a
-// tensor-core kernel), and the kernels both paths end in: the join of split items and the
-// accumulation of attention weights.
+// cache_fwd.cu -- attention over the 8-bit cache on fp32 FFMA (head dims above 256), and the kernels that the
+// other paths end in as well: the join of split items and the accumulation of attention weights.
 #include "cache_work.cuh"
 
 namespace attn {
@@ -42,8 +41,9 @@ __device__ __forceinline__ float warp_sum(float x) {
 // Four warps; each takes every fourth slice of 32 keys of the CTA's run.  Scores: one key per
 // lane, its codes read 16 at a time and multiplied with the rows' queries broadcast from shared
 // memory.  Output: four columns per lane (of each 128), the slice's probabilities broadcast from
-// shared memory.  NC: 128-column parts of D.  Bound by FFMA: 2 * 2 * 8 rows * D per 2 * D bytes is
-// 16 flops a byte, above what the fp32 pipes give at the memory's rate.
+// shared memory.  NC: 128-column parts of D.  16 flops a byte (2 * 2 * 8 rows * D per 2 * D bytes) would let
+// the fp32 pipes keep up with two thirds of the memory's rate, but each load of queries or probabilities
+// feeds four products only: 0.5 TB/s at D = 512 (one row of 114,000 keys, 8 kv heads, 4 queries to each).
 template <typename T, int KIND, int NC>
 __global__ void __launch_bounds__(kThreads) cache_fwd_simt_kernel(const __grid_constant__ FwdParams p) {
   extern __shared__ __align__(16) float sm[];
@@ -411,12 +411,7 @@ cudaError_t launch_simt_t(const FwdParams &p, cudaStream_t st) {
     kernel<<<p.max_ctas, kThreads, smem, st>>>(p);
     return counted(cudaGetLastError());
   };
-  switch ((D + 127) / 128) {
-    case 1: return go(cache_fwd_simt_kernel<T, KIND, 1>);
-    case 2: return go(cache_fwd_simt_kernel<T, KIND, 2>);
-    case 3: return go(cache_fwd_simt_kernel<T, KIND, 3>);
-    default: return go(cache_fwd_simt_kernel<T, KIND, 4>);
-  }
+  return D <= 384 ? go(cache_fwd_simt_kernel<T, KIND, 3>) : go(cache_fwd_simt_kernel<T, KIND, 4>);
 }
 
 }  // namespace

@@ -7,16 +7,21 @@
 namespace attn {
 namespace cache {
 
-bool mma_supported(int D) { return D == 64 || D == 128 || D == 256; }
+bool mma_supported(int D) { return D <= 256; }
+
+// The columns that the kernel for head dim D is compiled for.  Measured at 4 rows of some 115,000 keys, 8 kv
+// heads, 4 queries to each: D = 96 138 us (5.5 TB/s; one such row on FFMA 587), D = 192 300 us (5.1 TB/s), D = 80
+// 218 us (2.9 TB/s: rows of 80 bytes do not lie on the 32-byte sectors).
+int mma_columns(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 
 // Rows of a work item: 16, or 32 where there are more rows than that and the accumulators fit
 // (bf16, head dims up to 128), so that widening a code serves two row tiles.
 int mma_row_tile(int dtype, int D, int R) { return dtype == kBF16 && R > 16 && D <= 128 ? 32 : 16; }
 
-int mma_unit_shift(int D) { return D == 64 ? 8 : D == 128 ? 7 : 6; }  // four slices
+int mma_unit_shift(int D) { return D <= 64 ? 8 : D <= 128 ? 7 : 6; }  // four slices
 
 int mma_ctas_per_sm(int D, int row_tile) {
-  return row_tile == 32 || D == 256 ? 2 : 3;  // Cfg's CTAS
+  return row_tile == 32 || D > 128 ? 2 : 3;  // Cfg's CTAS
 }
 
 // How the work is spread.  A cluster of CTAs for each item (sequence, kv head, row tile) joins its parts in

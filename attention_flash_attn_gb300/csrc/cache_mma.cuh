@@ -1,5 +1,6 @@
-// cache_mma.cuh -- attention over the 8-bit cache on the tensor cores, head dims 64, 128 and 256
-// (instantiated for each kind of code in its own file).
+// cache_mma.cuh -- attention over the 8-bit cache on the tensor cores, head dims up to 256 (instantiated for
+// each kind of code in its own file).  Compiled for 64, 128 and 256 columns; a head dim in between takes the
+// next larger form, whose further columns TMA fills with zeros: they cost products, but no bytes of memory.
 //
 // Decoding reads 2 D bytes of codes per key and kv head and does 4 D flops per byte and query row, so
 // with the few rows of a step (G heads share a kv head) it is bound by memory; what can keep it from
@@ -16,8 +17,12 @@
 //     row's largest.
 //   - P is rounded to fp16 (half a step: 2^-11 of each probability, eight times finer than the bf16 result).
 //   - float queries take the same way in two terms each: q = hi + lo in fp16 (22 bits), p 2^14 = hi + lo, both
-//     terms multiplied into the same accumulators.  Twice the MMAs, which the memory hides; the fp32 pipes
-//     alone took 39 us where this takes 14 (9 ragged rows up to 9001 keys, one kv head).
+//     terms multiplied into the same accumulators.  Twice the MMAs; the FFMA kernel took 39 us where this
+//     takes 16 (9 ragged rows up to 9001 keys, one kv head).
+// Measured at 4 rows of some 115,000 keys, 8 kv heads, 4 bf16 queries to each: 4.9 TB/s at D = 64, 6.0 at 128, 6.5
+// at 256 (a copy reaches 6.8); float queries at D = 128 5.1.  Short calls are bound by the fixed parts, some 12 us:
+// launch, plan and first loads, the last run's end, the join.  With a row tile of 32, or D = 64 (half the bytes
+// per score), the warps' issue slots and latencies bound it, not the memory.
 #pragma once
 #include "cache_work.cuh"
 #include "tc_common.cuh"
@@ -384,7 +389,8 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
         for (int z = 0; z < kQW; ++z) {
           constexpr int kPerBlk = kQW / C::NB, kEl = 16 / (int)sizeof(T);
           raw_q[mt][y][z] = make_uint4(0, 0, 0, 0);
-          if (r < p.R) raw_q[mt][y][z] = *reinterpret_cast<const uint4 *>(row + (z / kPerBlk) * C::BLK + (z % kPerBlk) * kEl);
+          const int at = (z / kPerBlk) * C::BLK + (z % kPerBlk) * kEl;
+          if (r < p.R && at + t * (C::BLK / 4) < p.c.D) raw_q[mt][y][z] = *reinterpret_cast<const uint4 *>(row + at);
         }
       }
 
@@ -392,8 +398,9 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
     first = false;
 #pragma unroll
     for (int h = 0; h < C::NH; ++h) id_now[h] = id_nxt[h];
+    int filled = dead ? 0 : min(C::DEPTH, n_slices);  // slices asked for
 #pragma unroll 1
-    for (int s = 0; s < min(C::DEPTH, n_slices); ++s) issue(s, stage + s >= C::DEPTH ? stage + s - C::DEPTH : stage + s, id_now);
+    for (int s = 0; s < filled; ++s) issue(s, stage + s >= C::DEPTH ? stage + s - C::DEPTH : stage + s, id_now);
     fetch_scales();
     if (n_slices <= 0) load_next_ids(0);
 
@@ -479,7 +486,8 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
         fetch_scales();
       }
       uint8_t *const sk = base + (warp * C::DEPTH + stage) * C::STAGE, *const sv = sk + C::SK * D;
-      if (!dead) dead = !__all_sync(~0u, mbar_wait(bars + 8 * stage, (phases >> stage) & 1u, p.c.status));
+      // (Copies in flight are waited for even then: they end in this CTA's memory.)
+      if (x < filled) dead |= !mbar_wait_warp(bars + 8 * stage, (phases >> stage) & 1u, p.c.status);
       phases ^= 1u << stage;
       if ((x & 31) == 0) {
         take_scales();
@@ -710,6 +718,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
       __syncwarp();  // every lane has read the stage
       if (x + C::DEPTH < n_slices && !dead) {
         const int y = x + C::DEPTH;
+        ++filled;
         issue(y, stage, (y >> 5) == (x >> 5) ? id_now : id_nxt);
       }
       stage = stage + 1 == C::DEPTH ? 0 : stage + 1;
@@ -751,6 +760,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
 #pragma unroll 1
     for (int x = tid; x < rows * (D / 4); x += kThreads) {
       const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+      if (d >= p.c.D) continue;
       float2 ml[kWarps];
       float M = -CUDART_INF_F, L = 0.f;
 #pragma unroll
@@ -786,7 +796,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
         *reinterpret_cast<float4 *>(base + o_at(r, d) * 4) = v;
       } else {
         if (d == 0) p.ml_part[(size_t)run.slot * C::ROWS + r] = make_float2(M, L);
-        *reinterpret_cast<float4 *>(p.o_part + ((size_t)run.slot * C::ROWS + r) * D + d) = v;
+        *reinterpret_cast<float4 *>(p.o_part + ((size_t)run.slot * C::ROWS + r) * p.c.D + d) = v;
       }
     }
     if (one_of) {
@@ -795,6 +805,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
 #pragma unroll 1
       for (int x = rank * kThreads + tid; x < rows * (D / 4); x += p.cluster * kThreads) {
         const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+        if (d >= p.c.D) continue;
         const uint32_t ml_at = smem_u32(s_cta + r), v_at = smem_u32(base + o_at(r, d) * 4);
         float M = -CUDART_INF_F, L = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -838,8 +849,8 @@ cudaError_t launch_t(const FwdParams &p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   CUtensorMap km, vm;
   const int rows = p.c.page < C::SK ? p.c.page : C::SK;
-  if (!make_tmap_codes(&km, p.c.k, D, p.c.page, (long long)p.c.num_pages * p.c.Hkv, rows) ||
-      !make_tmap_codes(&vm, p.c.v, D, p.c.page, (long long)p.c.num_pages * p.c.Hkv, rows))
+  if (!make_tmap_codes(&km, p.c.k, p.c.D, p.c.page, (long long)p.c.num_pages * p.c.Hkv, C::BLK, rows) ||
+      !make_tmap_codes(&vm, p.c.v, p.c.D, p.c.page, (long long)p.c.num_pages * p.c.Hkv, C::BLK, rows))
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.cluster ? p.NG * p.c.Hkv * p.cluster : p.max_ctas));
@@ -856,15 +867,16 @@ cudaError_t launch_t(const FwdParams &p, cudaStream_t st) {
 }
 
 template <int KIND> cudaError_t launch_kind(const FwdParams &p, int dtype, cudaStream_t st) {
+  const int D = mma_columns(p.c.D);
   if (dtype == kF32) {
-    switch (p.c.D) {
+    switch (D) {
       case 64: return launch_t<float, KIND, 64, 1>(p, st);
       case 128: return launch_t<float, KIND, 128, 1>(p, st);
       default: return launch_t<float, KIND, 256, 1>(p, st);
     }
   }
   const bool two = p.row_tile == 32;
-  switch (p.c.D) {
+  switch (D) {
     case 64: return two ? launch_t<__nv_bfloat16, KIND, 64, 2>(p, st) : launch_t<__nv_bfloat16, KIND, 64, 1>(p, st);
     case 128: return two ? launch_t<__nv_bfloat16, KIND, 128, 2>(p, st) : launch_t<__nv_bfloat16, KIND, 128, 1>(p, st);
     default: return launch_t<__nv_bfloat16, KIND, 256, 1>(p, st);

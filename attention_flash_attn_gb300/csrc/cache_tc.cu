@@ -2,7 +2,7 @@
 // rows per kv head (drafts of several tokens, chunks of a prompt, many heads to a kv head).
 //
 // m16n8k16 products end at some 330 TFLOP/s here; with many rows the tensor cores' own path does more (570 TFLOP/s
-// for 2048 rows of 16111 keys at D = 128).  One CTA computes one 128-row tile of one (sequence, kv head) over one
+// for 2048 rows of 16111 keys at D = 128, 342 at D = 64).  One CTA computes one 128-row tile of one (sequence, kv head) over one
 // share of its keys, in tiles of 128 keys:
 //   warp 0        TMA: the tile's codes of K and V, page by page, and the scales of its 16-key groups into a
 //                 small ring;
@@ -606,8 +606,8 @@ template <int KIND, int D> cudaError_t launch_t(const FwdParams &p, cudaStream_t
   if (e != cudaSuccess) return e;
   CUtensorMap km, vm;
   const int rows = std::min(p.c.page, 64);
-  if (!make_tmap_codes(&km, p.c.k, D, p.c.page, (long long)p.c.num_pages * p.c.Hkv, rows) ||
-      !make_tmap_codes(&vm, p.c.v, D, p.c.page, (long long)p.c.num_pages * p.c.Hkv, rows))
+  if (!make_tmap_codes(&km, p.c.k, D, p.c.page, (long long)p.c.num_pages * p.c.Hkv, D, rows) ||
+      !make_tmap_codes(&vm, p.c.v, D, p.c.page, (long long)p.c.num_pages * p.c.Hkv, D, rows))
     return cudaErrorInvalidValue;
   kernel<<<(unsigned)(p.NG * p.c.Hkv * p.splits), kTcThreads, C::SMEM, st>>>(p, km, vm);
   return counted(cudaGetLastError());

@@ -24,17 +24,17 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 }  // namespace
 
-// [pages * heads, page, D] codes in boxes of box_rows rows by at most 128 columns, swizzled over the box
-// row's width (128 bytes, or 64 for D = 64).
-bool make_tmap_codes(CUtensorMap *m, const void *base, int D, int page, long long heads, int box_rows) {
+// [pages * heads, page, D] codes in boxes of box_rows rows by box_cols columns (64 or 128; columns past D are
+// filled with zeros), swizzled over the box row's width.
+bool make_tmap_codes(CUtensorMap *m, const void *base, int D, int page, long long heads, int box_cols, int box_rows) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)page, (cuuint64_t)heads};
   cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)D * page};
-  cuuint32_t box[3] = {(cuuint32_t)(D < 128 ? D : 128), (cuuint32_t)box_rows, 1};
+  cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -69,7 +69,7 @@ class Case:
             hid = None if hidden is None else hidden[b]
             if hid is not None:
                 kk, vv = torch.where(hid[:, None, None], 0.0, kk), torch.where(hid[:, None, None], 0.0, vv)
-            vs = ref.gather_scale(self.vs, self.table[b], n, self.page) if self.D in (64, 128, 256) or half else None
+            vs = ref.gather_scale(self.vs, self.table[b], n, self.page) if self.D <= 256 or half else None
             o, lse, w, pv, mag = ref.attend(self.q[b].double(), kk, vv, sink=self.sink if sink else None, hidden=hid, vs=vs,
                                             terms=1 if half else 2, **kw)
             e, rel = ref.bounds(self.D, n, mag, kw.get("softcap", 0.0), half)
@@ -100,7 +100,22 @@ def test_single_tokens(dtype, D, page, kind):
     c = Case(ODD, D=D, page=page, kind=kind, dtype=dtype, seed=D + page)
     c.check(*c.run())
     path = fa().attn_cache_path_name(c.cuda["q"], c.cache, c.cuda["table"], c.cuda["lengths"])
-    assert path == ("mma" if D in (64, 128, 256) else "simt")
+    assert path == ("mma" if D <= 256 else "simt")
+
+
+@pytest.mark.parametrize("kind", [E4M3, INT8])
+@pytest.mark.parametrize("dtype,D,page,G,Sq", [(BF16, 16, 16, 4, 1), (BF16, 32, 128, 4, 6), (BF16, 48, 32, 5, 1), (BF16, 80, 64, 4, 1),
+                                               (BF16, 96, 16, 8, 5), (BF16, 112, 128, 3, 40), (BF16, 144, 16, 4, 1),
+                                               (BF16, 160, 64, 2, 9), (BF16, 192, 128, 8, 1), (BF16, 240, 32, 1, 1),
+                                               (F32, 48, 64, 4, 1), (F32, 96, 32, 8, 3), (F32, 208, 16, 4, 1)])
+def test_head_dims_between_those_compiled(dtype, D, page, G, Sq, kind):
+    """One cluster to an item, and (the second case) a split over the grid with the join."""
+    for lengths, Hkv in ((ODD, 2), ([9001, 5] + [3000] * 30, 6)):
+        c = Case(lengths, Sq=Sq, Hq=G * Hkv, Hkv=Hkv, D=D, page=page, kind=kind, dtype=dtype, seed=D + page)
+        w = c.cuda["w"].clone()
+        out = c.run(sink=c.cuda["sink"], window=700, softcap=15.0, weights=w)
+        c.check(out[0], out[1], w, rows=[0, 1, 4], sink=True, window=700, softcap=15.0)
+        c.check(*c.run(), rows=[0, 2])
 
 
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 1), (5, 5), (16, 2), (20, 2), (32, 1), (40, 1), (64, 8), (96, 3)])
@@ -305,7 +320,7 @@ def test_elements_of_a_query_far_apart(D):
     c.check(*c.run(scale=2.0 ** -13), scale=2.0 ** -13)
 
 
-@pytest.mark.parametrize("dtype,D", [(BF16, 64), (BF16, 128), (BF16, 256), (F32, 128)])
+@pytest.mark.parametrize("dtype,D", [(BF16, 64), (BF16, 128), (BF16, 256), (F32, 128), (BF16, 80), (BF16, 144), (F32, 48)])
 def test_nan_in_the_last_tokens_reaches_only_the_rows_that_see_them(dtype, D):
     c = Case([70], Sq=6, Hq=4, Hkv=2, D=D, dtype=dtype)
     p, slot = int(c.table[0, 68 // 64]), 68 % 64
