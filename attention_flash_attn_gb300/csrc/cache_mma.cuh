@@ -715,7 +715,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
               }
           }
       }
-      __syncwarp();  // every lane has read the stage
+      __syncwarp();  // every lane has read the stage (and multiplied what it read: the loads have come)
       if (x + C::DEPTH < n_slices && !dead) {
         const int y = x + C::DEPTH;
         ++filled;

@@ -377,7 +377,13 @@ cache_tc_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUt
           }
           fence_async_smem();  // (codes that mark_nans wrote, before the next load)
         }
-        mbar_arrive(c_empty(kv));
+        // The codes' place is given away only once they have come: a load may be held up longer than the arrival
+        // and the next tile's copy take (by stores of scores in the same unit), and nothing orders it before a copy
+        // by TMA.  So the barrier's address hangs on a word of each load (p.cluster is 0 here).
+        uint32_t come = 0;
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) come |= u[y].x;
+        mbar_arrive(c_empty(kv) + (come & (uint32_t)p.cluster));
         // Chunks 2 (c % 4) and the next of block c / 4; the lanes of the second block store them the other way
         // round, so that eight lanes meet all banks.
         uint8_t *const blk = to + (c / 4) * (kBN * 128);
