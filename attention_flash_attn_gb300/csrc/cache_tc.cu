@@ -1,5 +1,6 @@
-// cache_tc.cu -- attention over the 8-bit cache with tcgen05: bf16 queries, head dims 64 and 128, many query
-// rows per kv head (drafts of several tokens, chunks of a prompt, many heads to a kv head).
+// cache_tc.cu -- attention over the 8-bit cache with tcgen05: bf16 queries, head dims up to 128 (compiled for 64
+// and 128 columns, those past the head dim filled with zeros), many query rows per kv head (drafts of several
+// tokens, chunks of a prompt, many heads to a kv head).
 //
 // m16n8k16 products end at some 330 TFLOP/s here; with many rows the tensor cores' own path does more (570 TFLOP/s
 // for 2048 rows of 16111 keys at D = 128, 342 at D = 64).  One CTA computes one 128-row tile of one (sequence, kv head) over one
@@ -219,6 +220,7 @@ cache_tc_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUt
       return pos < key1 ? page_of(p.c, b, pos) : -1;
     };
     id_nxt = load_id(0);
+    int asked[2] = {0, 0};  // tiles of K, of V
     for (int j = 0; ok && j < n; ++j) {
       const int sub = j & 3;
       if (sub == 0) {
@@ -241,6 +243,7 @@ cache_tc_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUt
           break;
         }
         if (lane == 0) mbar_arrive_expect_tx(c_full(kv), bytes);
+        ++asked[kv];
         __syncwarp();
         if (lead)
           tma_load_3d(sbase + C::OFF_C + kv * C::CODES + grp * 16 * D, kv ? &vmap : &kmap, c_full(kv), 0, pos & (p.c.page - 1),
@@ -265,6 +268,9 @@ cache_tc_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUt
         }
       }
     }
+    // A wait gave up: the copies in flight end in this CTA's memory, so they are waited for.
+    for (int kv = 0; !ok && kv < 2; ++kv)
+      if (asked[kv]) mbar_wait_warp(c_full(kv), (asked[kv] - 1) & 1, p.c.status);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (n > 0) {
@@ -313,7 +319,7 @@ cache_tc_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUt
 #pragma unroll
       for (int c = 0; c < D / 8; ++c) {
         raw[c] = make_uint4(0, 0, 0, 0);
-        if (t < rows)
+        if (t < rows && c * 8 < p.c.D)
           raw[c] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + b * p.q_sb + i * p.q_ss + h * p.q_sh + c * 8);
       }
 #pragma unroll
@@ -582,14 +588,16 @@ cache_tc_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUt
           uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.O) + o_row(p, b, hk, r0 + r) + c * 32);
 #pragma unroll
           for (int x = 0; x < 4; ++x)
-            dst[x] = make_uint4(pack_bf16(__uint_as_float(o[8 * x]), __uint_as_float(o[8 * x + 1])),
-                                pack_bf16(__uint_as_float(o[8 * x + 2]), __uint_as_float(o[8 * x + 3])),
-                                pack_bf16(__uint_as_float(o[8 * x + 4]), __uint_as_float(o[8 * x + 5])),
-                                pack_bf16(__uint_as_float(o[8 * x + 6]), __uint_as_float(o[8 * x + 7])));
+            if (c * 32 + 8 * x < p.c.D)
+              dst[x] = make_uint4(pack_bf16(__uint_as_float(o[8 * x]), __uint_as_float(o[8 * x + 1])),
+                                  pack_bf16(__uint_as_float(o[8 * x + 2]), __uint_as_float(o[8 * x + 3])),
+                                  pack_bf16(__uint_as_float(o[8 * x + 4]), __uint_as_float(o[8 * x + 5])),
+                                  pack_bf16(__uint_as_float(o[8 * x + 6]), __uint_as_float(o[8 * x + 7])));
         } else if (row_ok) {
-          uint4 *dst = reinterpret_cast<uint4 *>(p.o_part + part * D + c * 32);
+          uint4 *dst = reinterpret_cast<uint4 *>(p.o_part + part * p.c.D + c * 32);
 #pragma unroll
-          for (int x = 0; x < 8; ++x) dst[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          for (int x = 0; x < 8; ++x)
+            if (c * 32 + 4 * x < p.c.D) dst[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
         }
         __syncwarp();  // together into the next load from TMEM
       }
@@ -612,8 +620,8 @@ template <int KIND, int D> cudaError_t launch_t(const FwdParams &p, cudaStream_t
   if (e != cudaSuccess) return e;
   CUtensorMap km, vm;
   const int rows = std::min(p.c.page, 64);
-  if (!make_tmap_codes(&km, p.c.k, D, p.c.page, (long long)p.c.num_pages * p.c.Hkv, D, rows) ||
-      !make_tmap_codes(&vm, p.c.v, D, p.c.page, (long long)p.c.num_pages * p.c.Hkv, D, rows))
+  if (!make_tmap_codes(&km, p.c.k, p.c.D, p.c.page, (long long)p.c.num_pages * p.c.Hkv, D, rows) ||
+      !make_tmap_codes(&vm, p.c.v, p.c.D, p.c.page, (long long)p.c.num_pages * p.c.Hkv, D, rows))
     return cudaErrorInvalidValue;
   kernel<<<(unsigned)(p.NG * p.c.Hkv * p.splits), kTcThreads, C::SMEM, st>>>(p, km, vm);
   return counted(cudaGetLastError());
@@ -627,8 +635,9 @@ int tc_unit_shift() { return 7; }
 // From how many rows per kv head this kernel is taken.  Measured against the kernel of cache_mma.cuh (us, this /
 // that), D = 128 with 8 kv heads: 16 ragged rows up to 8192 keys, 36 query rows 128 / 98, 64 131 / 109, 96
 // 136 / 159, 128 141 / 209; one row of 16111 keys, 96 rows 37 / 41, 2048 rows 234 / 430.  D = 64, where a tile's
-// MMAs are half and its softmax is not: 160 rows 49 / 37, 512 78 / 72, 1024 125 / 129, 2048 193 / 244.
-bool tc_supported_rows(int dtype, int D, int R) { return dtype == kBF16 && ((D == 128 && R > 64) || (D == 64 && R > 512)); }
+// MMAs are half and its softmax is not: 160 rows 49 / 37, 512 78 / 72, 1024 125 / 129, 2048 193 / 244.  A head dim in
+// between takes the time of the next larger one on either (2048 rows at D = 96 231 here).
+bool tc_supported_rows(int dtype, int D, int R) { return dtype == kBF16 && D <= 128 && R > (D > 64 ? 64 : 512); }
 
 // Shares of an item's keys, one CTA each, one CTA per SM: enough for three waves (the block scheduler then
 // evens ragged rows out), of at least four tiles.
@@ -641,7 +650,7 @@ int tc_splits(const FwdParams &p) {
 }
 
 cudaError_t launch_fwd_tc(const FwdParams &p, int kind, cudaStream_t st) {
-  if (p.c.D == 64) return kind == ATTN_CACHE_E4M3 ? launch_t<ATTN_CACHE_E4M3, 64>(p, st) : launch_t<ATTN_CACHE_INT8, 64>(p, st);
+  if (p.c.D <= 64) return kind == ATTN_CACHE_E4M3 ? launch_t<ATTN_CACHE_E4M3, 64>(p, st) : launch_t<ATTN_CACHE_INT8, 64>(p, st);
   return kind == ATTN_CACHE_E4M3 ? launch_t<ATTN_CACHE_E4M3, 128>(p, st) : launch_t<ATTN_CACHE_INT8, 128>(p, st);
 }
 

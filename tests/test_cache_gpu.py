@@ -241,6 +241,18 @@ def test_many_rows_and_nan_in_the_last_tokens(D):
     assert torch.isnan(O[0, sees:, G:]).all() and torch.isnan(LSE[0, G:, sees:]).all()
 
 
+@pytest.mark.parametrize("D,G,Sq", [(16, 8, 80), (48, 4, 150), (80, 3, 23), (96, 8, 40), (112, 130, 1)])
+@pytest.mark.parametrize("kind", [E4M3, INT8])
+def test_many_rows_at_head_dims_between(D, G, Sq, kind):
+    for lengths, kw in (([1031, 0, 77, 500], dict(softcap=20.0)), ([9000, 9], dict(causal=True, window=400))):
+        c = Case(lengths, Sq=Sq, Hq=2 * G, Hkv=2, D=D, page=32, kind=kind, seed=D)
+        t = c.cuda
+        assert fa().attn_cache_path_name(t["q"], c.cache, t["table"], t["lengths"], **kw) == "tc"
+        w = t["w"].clone()
+        out = c.run(sink=t["sink"], weights=w, **kw)
+        c.check(out[0], out[1], w, sink=True, **kw)
+
+
 @pytest.mark.parametrize("dtype,D", [(BF16, 64), (BF16, 128), (F32, 64)])
 def test_many_short_sequences(dtype, D):
     g = torch.Generator().manual_seed(1)
