@@ -365,22 +365,28 @@ cache_tc_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUt
         uint4 u[kPer];
 #pragma unroll
         for (int y = 0; y < kPer; ++y) u[y] = *reinterpret_cast<const uint4 *>(codes + code_at<D>(row0 + y * step, c));
-        if (partial) {  // values only: what no row sees is 0, and so is a NaN, after it is marked
+        if (partial) {  // values only: a NaN is marked and becomes 0, and so does what no row sees
+          auto hidden = [&](int row) { return pos + row >= key1 || ((hide >> (row >> 4)) & 1u); };
+          if (KIND == ATTN_CACHE_E4M3) {
+            unsigned any = 0;
 #pragma unroll
-          for (int y = 0; y < kPer; ++y) {
-            const int row = row0 + y * step;
-            if (pos + row >= key1 || ((hide >> (row >> 4)) & 1u)) {
-              u[y] = make_uint4(0, 0, 0, 0);
-            } else if (KIND == ATTN_CACHE_E4M3) {
-              const uint32_t any = ((u[y].x & 0x7f7f7f7fu) + 0x01010101u) | ((u[y].y & 0x7f7f7f7fu) + 0x01010101u) |
-                                   ((u[y].z & 0x7f7f7f7fu) + 0x01010101u) | ((u[y].w & 0x7f7f7f7fu) + 0x01010101u);
-              if (any & 0x80808080u) {
-                uint8_t *at = codes + code_at<D>(row, c);
-                mark_nans<D>(p, at, pos + row, c * 16, range.len, r0, rows, s_nan, misc + 1);
-                u[y] = *reinterpret_cast<const uint4 *>(at);
+            for (int y = 0; y < kPer; ++y)  // (a byte of 0x7f, and no other, carries into its top bit)
+              any |= hidden(row0 + y * step) ? 0u
+                                             : ((u[y].x & 0x7f7f7f7fu) + 0x01010101u) | ((u[y].y & 0x7f7f7f7fu) + 0x01010101u) |
+                                                   ((u[y].z & 0x7f7f7f7fu) + 0x01010101u) | ((u[y].w & 0x7f7f7f7fu) + 0x01010101u);
+            if (any & 0x80808080u) {
+#pragma unroll 1
+              for (int y = 0; y < kPer; ++y) {
+                const int row = row0 + y * step;
+                if (!hidden(row)) mark_nans<D>(p, codes + code_at<D>(row, c), pos + row, c * 16, range.len, r0, rows, s_nan, misc + 1);
               }
+#pragma unroll
+              for (int y = 0; y < kPer; ++y) u[y] = *reinterpret_cast<const uint4 *>(codes + code_at<D>(row0 + y * step, c));
             }
           }
+#pragma unroll
+          for (int y = 0; y < kPer; ++y)
+            if (hidden(row0 + y * step)) u[y] = make_uint4(0, 0, 0, 0);
           fence_async_smem();  // (codes that mark_nans wrote, before the next load)
         }
         // The codes' place is given away only once they have come: a load may be held up longer than the arrival
@@ -513,16 +519,20 @@ cache_tc_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUt
         uint32_t pk[16];
 #pragma unroll
         for (int g = 2 * q; g < 2 * q + 2; ++g) {
-          const float ref = lv[g] - mr;
-          float sum = 0.f;
+          const uint64_t f2 = f2_splat(f[g]), ref2 = f2_splat(lv[g] - mr);
+          uint64_t sum = 0;  // (two floats)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float p0 = ex2_approx(fmaf(f[g], __uint_as_float(xr[16 * g + 2 * e]), ref));
-            const float p1 = ex2_approx(fmaf(f[g], __uint_as_float(xr[16 * g + 2 * e + 1]), ref));
-            sum += p0 + p1;
+            float p0, p1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(xr[16 * g + 2 * e]), __uint_as_float(xr[16 * g + 2 * e + 1])), f2, ref2), p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            sum = f2_add(sum, f2_pack(p0, p1));
             pk[8 * (g - 2 * q) + e] = pack_h2(p0, p1);
           }
-          l = fmaf(sum, ex2_approx(-lv[g]), l);
+          float s0, s1;
+          f2_unpack(sum, s0, s1);
+          l = fmaf(s0 + s1, ex2_approx(-lv[g]), l);
         }
         __syncwarp();
         tmem_st16(sa + 16 * q, pk);
@@ -639,14 +649,26 @@ int tc_unit_shift() { return 7; }
 // between takes the time of the next larger one on either (2048 rows at D = 96 231 here).
 bool tc_supported_rows(int dtype, int D, int R) { return dtype == kBF16 && D <= 128 && R > (D > 64 ? 64 : 512); }
 
-// Shares of an item's keys, one CTA each, one CTA per SM: enough for three waves (the block scheduler then
-// evens ragged rows out), of at least four tiles.
+// Shares of an item's keys, one CTA each, one CTA per SM, of at least four tiles.  One sequence: as many as end first,
+// by a count of tiles (kStart: a CTA's start and end).  A batch, whose lengths the host does not know: enough for
+// three waves, so that the block scheduler evens ragged rows out.  One row of 16111 keys (us, by the count / by three
+// waves): 2048 rows 186 / 228, 256 41 / 72, 96 29 / 39.
 int tc_splits(const FwdParams &p) {
+  constexpr long long kStart = 6;
   const long long items = (long long)p.NG * p.c.Hkv, sms = device_sm_count();
   long long keys = (long long)p.c.max_pages << p.c.page_shift;
   if (p.window > 0) keys = std::min(keys, (long long)p.window + p.Sq);
-  const long long most = std::max(1LL, (keys + 4 * kBN - 1) / (4 * kBN));
-  return (int)std::max(1LL, std::min(most, (3 * sms + items - 1) / items));
+  const long long tiles = std::max(1LL, (keys + kBN - 1) / kBN), most = (tiles + 3) / 4;
+  if (p.c.B > 1) return (int)std::min(most, (3 * sms + items - 1) / items);
+  long long best = 0, at = 1;
+  for (long long s = 1; s <= most && (s == 1 || items * (s - 1) < 4 * sms); ++s) {
+    const long long t = (items * s + sms - 1) / sms * ((tiles + s - 1) / s + kStart);
+    if (s == 1 || t < best) {
+      best = t;
+      at = s;
+    }
+  }
+  return (int)at;
 }
 
 cudaError_t launch_fwd_tc(const FwdParams &p, int kind, cudaStream_t st) {
