@@ -99,8 +99,8 @@ int validate(const attn_cache *c, const attn_cache_seqs *s, const attn_cache_fwd
   return ATTN_OK;
 }
 
-bool use_tc(const attn_cache *c, const attn_cache_fwd_args *a) {
-  return tc_supported_rows(a->dtype, c->D, a->Hq / c->Hkv * a->Sq);
+bool use_tc(const attn_cache *c, const attn_cache_seqs *s, const attn_cache_fwd_args *a) {
+  return tc_supported_rows(a->dtype, c->D, (int)std::min((long long)INT_MAX, (long long)(a->Hq / c->Hkv) * a->Sq), s->B);
 }
 bool use_mma(const attn_cache *c) { return mma_supported(c->D); }
 
@@ -116,7 +116,7 @@ FwdParams fwd_params(const attn_cache *c, const attn_cache_seqs *s, const attn_c
   p.Hq = a->Hq;
   p.G = a->Hq / c->Hkv;
   p.R = p.G * a->Sq;
-  const bool tc = use_tc(c, a), mma = !tc && use_mma(c);
+  const bool tc = use_tc(c, s, a), mma = !tc && use_mma(c);
   p.row_tile = tc ? tc_row_tile() : mma ? mma_row_tile(a->dtype, c->D, p.R) : simt_row_tile();
   p.RT = (p.R + p.row_tile - 1) / p.row_tile;
   p.NG = s->B * p.RT;
@@ -212,7 +212,7 @@ size_t attn_cache_fwd_workspace_size(const attn_cache *c, const attn_cache_seqs 
 
 const char *attn_cache_path_name(const attn_cache *c, const attn_cache_seqs *s, const attn_cache_fwd_args *a) {
   if (validate(c, s, a) != ATTN_OK) return "";
-  return use_tc(c, a) ? "tc" : use_mma(c) ? "mma" : "simt";
+  return use_tc(c, s, a) ? "tc" : use_mma(c) ? "mma" : "simt";
 }
 
 int attn_cache_fwd(const attn_cache *c, const attn_cache_seqs *s, const attn_cache_fwd_args *a, void *O,

@@ -2,9 +2,9 @@
 // and 128 columns, those past the head dim filled with zeros), many query rows per kv head (drafts of several
 // tokens, chunks of a prompt, many heads to a kv head).
 //
-// m16n8k16 products end at some 330 TFLOP/s here; with many rows the tensor cores' own path does more (570 TFLOP/s
-// for 2048 rows of 16111 keys at D = 128, 342 at D = 64).  One CTA computes one 128-row tile of one (sequence, kv head) over one
-// share of its keys, in tiles of 128 keys:
+// m16n8k16 products end at some 330 TFLOP/s here; with many rows the tensor cores' own path does more (715 TFLOP/s
+// for 2048 rows of 16111 keys at D = 128, 410 at D = 64).  One CTA computes one 128-row tile of one (sequence, kv
+// head) over one share of its keys, in tiles of 128 keys:
 //   warp 0        TMA: the tile's codes of K and V, page by page, and the scales of its 16-key groups into a
 //                 small ring;
 //   warp 1        MMA issuer: S_j = Q K_j^T into one of two TMEM buffers, O += P_{j-1} V_{j-1} with P in TMEM;
@@ -17,7 +17,9 @@
 // 3500 clocks a tile: the softmax warps are busy for 2900 of them (the exponentials alone, 128 x 128 at 16 a
 // clock, take 1024) and the converters for 2700; the two MMAs take 544 each.  Twice the converter warps, with
 // registers moved to the softmax (640 threads), and converters for K and V apart were slower (258 and 270 us
-// against 233): shared memory is what they share.
+// against 233): shared memory is what they share.  So was a form of 256 rows to a CTA, each of whose two groups of
+// warps had 128 rows or every second tile, with scores in one buffer each: 176 us where this took 194 without a
+// cap, but 405 against 342 with one, and 47 against 43 at 256 rows.
 #include <algorithm>
 
 #include "cache_work.cuh"
@@ -643,11 +645,13 @@ int tc_row_tile() { return kBM; }
 int tc_unit_shift() { return 7; }
 
 // From how many rows per kv head this kernel is taken.  Measured against the kernel of cache_mma.cuh (us, this /
-// that), D = 128 with 8 kv heads: 16 ragged rows up to 8192 keys, 36 query rows 128 / 98, 64 131 / 109, 96
-// 136 / 159, 128 141 / 209; one row of 16111 keys, 96 rows 37 / 41, 2048 rows 234 / 430.  D = 64, where a tile's
-// MMAs are half and its softmax is not: 160 rows 49 / 37, 512 78 / 72, 1024 125 / 129, 2048 193 / 244.  A head dim in
-// between takes the time of the next larger one on either (2048 rows at D = 96 231 here).
-bool tc_supported_rows(int dtype, int D, int R) { return dtype == kBF16 && D <= 128 && R > (D > 64 ? 64 : 512); }
+// that) with 8 kv heads.  D = 128: 16 ragged rows up to 8192 keys, 36 query rows 128 / 98, 64 131 / 109, 96
+// 136 / 159, 128 141 / 209; one row of 16111 keys, 64 rows 24 / 28 (with a cap 32 / 30), 2048 186 / 430; one of
+// 3000, 64 rows 17 / 16.  D = 64, where a tile's MMAs are half and its softmax is not: the ragged rows, 160 query
+// rows 49 / 37, 512 78 / 72, 1024 125 / 129, 2048 193 / 244; one row of 16111 keys, 128 rows 21 / 26 (with a cap
+// 29 / 31), 256 31 / 47, 512 50 / 71; one of 3000, 128 rows 16 / 13, 256 20 / 16, 384 23 / 22, 512 20 / 23.  A head
+// dim in between takes the time of the next larger one on either.
+bool tc_supported_rows(int dtype, int D, int R, int B) { return dtype == kBF16 && D <= 128 && R > (D > 64 ? 64 : B > 1 ? 512 : 256); }
 
 // Shares of an item's keys, one CTA each, one CTA per SM, of at least four tiles.  One sequence: as many as end first,
 // by a count of tiles (kStart: a CTA's start and end).  A batch, whose lengths the host does not know: enough for
