@@ -18,6 +18,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <string>
+#include <utility>
 
 #include "../../include/attn_cache_gb300.h"
 
@@ -140,6 +141,18 @@ void weight_rows(const char *where, const char *name, const at::Tensor &t, int64
   same_device(where, c, t);
 }
 
+// Weights that a call writes: rows of [B, Hkv] that keep off one another in their first `room` elements.
+void written_rows(const char *where, const char *name, const at::Tensor &t, int64_t B, int64_t room, const Cache &c) {
+  weight_rows(where, name, t, B, room, c);
+  int64_t n[2] = {t.size(0), t.size(1)}, s[2] = {t.stride(0), t.stride(1)};
+  if (s[0] < s[1]) {
+    std::swap(n[0], n[1]);
+    std::swap(s[0], s[1]);
+  }
+  if ((n[1] > 1 && s[1] < room) || (n[0] > 1 && s[0] < (n[1] > 1 ? (n[1] - 1) * s[1] : 0) + room))
+    raise(PyExc_ValueError, "%s: the rows of %s must not overlap", where, name);
+}
+
 // A given output, checked, or a new one.
 at::Tensor output(const char *where, const char *name, PyObject *o, at::IntArrayRef shape, at::ScalarType ty, const Cache &c) {
   if (o == Py_None) return at::empty(shape, at::TensorOptions().dtype(ty).device(c.device()));
@@ -211,7 +224,7 @@ PyObject *append(PyObject *const *a, Py_ssize_t n) {
   }
   if (a[7] != Py_None) {
     const at::Tensor &t = tensor(where, "weights", a[7]);
-    weight_rows(where, "weights", t, B, (int64_t)s.max_pages * c.c->page_size, c);
+    written_rows(where, "weights", t, B, (int64_t)s.max_pages * c.c->page_size, c);
     g.weights = static_cast<float *>(t.data_ptr());
     g.weights_stride_b = t.stride(0);
     g.weights_stride_h = t.stride(1);
@@ -251,7 +264,7 @@ void fwd_args(const char *where, const Cache &c, PyObject *const *a, attn_cache_
     const at::Tensor &w = tensor(where, "weights", a[11]);
     weight_rows(where, "weights", w, B, room, c);
     const at::Tensor &o = a[12] == Py_None ? w : tensor(where, "weights_out", a[12]);
-    weight_rows(where, "weights_out", o, B, room, c);
+    written_rows(where, "weights_out", o, B, room, c);
     if (w.strides() != o.strides()) raise(PyExc_ValueError, "%s: weights and weights_out must have the same strides", where);
     g->weights = static_cast<const float *>(w.data_ptr());
     g->weights_out = static_cast<float *>(o.data_ptr());

@@ -76,6 +76,16 @@ bool strides_ok(int dtype, std::initializer_list<int64_t> st) {
   return true;
 }
 
+// Rows of accumulated weights that a call writes, [B, Hkv, max_pages * page_size], keep off one another.
+bool rows_apart(const attn_cache *c, const attn_cache_seqs *s, int64_t sb, int64_t sh) {
+  const int64_t room = (int64_t)s->max_pages * c->page_size;
+  if (s->B <= 1) return c->Hkv <= 1 || sh >= room;
+  if (c->Hkv <= 1) return sb >= room;
+  const bool nested = sb >= sh;  // heads within sequences
+  const int64_t in = nested ? sh : sb, out = nested ? sb : sh, count = nested ? c->Hkv : s->B;
+  return in >= room && out >= (count - 1) * in + room;
+}
+
 int validate(const attn_cache *c, const attn_cache_seqs *s, const attn_cache_fwd_args *a) {
   const int e = validate(c, s);
   if (e != ATTN_OK) return e;
@@ -88,6 +98,7 @@ int validate(const attn_cache *c, const attn_cache_seqs *s, const attn_cache_fwd
   if (!aligned4(a->weights) || !aligned4(a->weights_out) || !aligned4(a->sink)) return ATTN_ERR_INVALID;
   if (a->weights && (a->weights_stride_b < 0 || a->weights_stride_h < 0)) return ATTN_ERR_INVALID;
   if (s->B == 0 || a->Sq == 0) return ATTN_OK;
+  if (a->weights && !rows_apart(c, s, a->weights_stride_b, a->weights_stride_h)) return ATTN_ERR_INVALID;
   if (!a->q || !aligned16(a->q)) return ATTN_ERR_INVALID;
   if (!strides_ok(a->dtype, {a->q_stride_b, a->q_stride_s, a->q_stride_h})) return ATTN_ERR_INVALID;
   const long long R = (long long)(a->Hq / c->Hkv) * a->Sq;
@@ -180,6 +191,7 @@ int attn_cache_append(const attn_cache *c, const attn_cache_seqs *s, const attn_
   if (!aligned4(a->counts) || !aligned4(a->lengths_out) || !aligned4(a->weights)) return ATTN_ERR_INVALID;
   if (a->lengths_out && a->lengths_out == s->lengths) return ATTN_ERR_INVALID;
   if (a->weights && (a->weights_stride_b < 0 || a->weights_stride_h < 0)) return ATTN_ERR_INVALID;
+  if (a->weights && !rows_apart(c, s, a->weights_stride_b, a->weights_stride_h)) return ATTN_ERR_INVALID;
   if (a->S > 0) {
     if (!a->k || !a->v || !aligned16(a->k) || !aligned16(a->v)) return ATTN_ERR_INVALID;
     if (!strides_ok(a->dtype, {a->k_stride_b, a->k_stride_s, a->k_stride_h, a->v_stride_b, a->v_stride_s, a->v_stride_h}))

@@ -83,7 +83,7 @@ typedef struct {
     const int32_t *counts;     /* [B] in 0 .. S (clamped), or NULL: S for every sequence  */
     int32_t *lengths_out;      /* [B] or NULL                                             */
     /* Optional accumulated weights [B, Hkv, >= max_pages * page_size] float with element
-     * strides: those of the new tokens are set to 0.                                      */
+     * strides (rows may not overlap): those of the new tokens are set to 0.               */
     float *weights;
     int64_t weights_stride_b, weights_stride_h;
 } attn_cache_append_args;
@@ -103,8 +103,9 @@ int attn_cache_append(const attn_cache *c, const attn_cache_seqs *s, const attn_
  * weights_out, if given, takes for every cached key j < lengths[b]
  *   weights_out[b, hkv, j] = weights[b, hkv, j] + sum over the queries i and the heads h of kv
  *                            head hkv of exp(t_ij - LSE_i)                       (0 if unseen)
- * in float, summed in a fixed order (no atomics).  weights == weights_out adds in place; both
- * are [B, Hkv, >= max_pages * page_size] with the same element strides.
+ * in float, summed in a fixed order (no atomics).  weights == weights_out adds in place, else the
+ * two may not overlap; both are [B, Hkv, >= max_pages * page_size] with the same element strides,
+ * whose rows may not overlap.  Nor may O, LSE and the workspace overlap anything that the call reads.
  *
  * Head dims up to 256 run on the tensor cores with the codes widened to fp16 (exact) and
  * the queries scaled per row by a power of two into fp16: bf16 queries exactly (elements within

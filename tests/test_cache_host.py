@@ -141,6 +141,18 @@ def test_outputs_and_workspace_are_checked(capi):
     assert L.attn_launch_counter() == n
 
 
+def test_rows_of_written_weights_that_overlap_are_refused(capi):
+    s = seq_args(capi)
+    room = s.max_pages * 64
+    for sb, sh, ok in ((2 * room, room, True), (room, 2 * room, True), (0, room, False), (room, 0, False), (2 * room - 1, room, False),
+                       (room, room, False)):
+        f = fwd_args(capi, weights=FAKE, weights_out=FAKE, weights_stride_b=sb, weights_stride_h=sh)
+        assert (calls(capi, cache_args(capi), s, f=f)[3]() > 0) == ok, (sb, sh)
+        if not ok:
+            a = append_args(capi, weights=FAKE, weights_stride_b=sb, weights_stride_h=sh)
+            assert calls(capi, cache_args(capi), s, f=f, a=a)[0]() == 1 and calls(capi, cache_args(capi), s, f=f, a=a)[1]() == 1
+
+
 def test_scores_are_part_of_the_workspace_only_with_weights(capi):
     L, r = capi.lib(), ctypes.byref
     c, s = cache_args(capi), seq_args(capi)
@@ -242,6 +254,12 @@ def test_attention_arguments_of_the_binding():
         go(weights_out=w)
     with pytest.raises(ValueError, match="strides"):
         go(weights=w, weights_out=torch.zeros(2, 2, 130)[:, :, :128])
+    for bad in (torch.zeros(1, 2, 128).expand(2, 2, 128), torch.zeros(2, 1, 128).expand(2, 2, 128),
+                torch.zeros(400).as_strided((2, 2, 128), (200, 100, 1)), torch.zeros(400).as_strided((2, 2, 128), (130, 130, 1))):
+        with pytest.raises(ValueError, match="weights.* must not overlap"):
+            go(weights=bad)
+    for good in (torch.zeros(2, 2, 128).transpose(0, 1), torch.zeros(600).as_strided((2, 2, 128), (128, 300, 1))):
+        assert go(weights=good)
     for kw, what in ((dict(out=torch.zeros(2, 1, 4, 128)), "out"), (dict(lse=torch.zeros(2, 4)), "lse")):
         with pytest.raises(ValueError, match=what):
             fa.attn_cache_fwd(q, c, table, lengths, **kw)
@@ -263,6 +281,8 @@ def test_append_arguments_of_the_binding():
         fa.attn_cache_append(c, k, k, table, lengths, counts=torch.tensor([1, 1]))
     with pytest.raises(ValueError, match="weights"):
         fa.attn_cache_append(c, k, k, table, lengths, weights=torch.zeros(2, 2, 64))
+    with pytest.raises(ValueError, match="must not overlap"):
+        fa.attn_cache_append(c, k, k, table, lengths, weights=torch.zeros(1, 2, 128).expand(2, 2, 128))
 
 
 def test_eviction_arguments_of_the_binding():
