@@ -157,7 +157,8 @@ def test_scores_are_part_of_the_workspace_only_with_weights(capi):
     L, r = capi.lib(), ctypes.byref
     c, s = cache_args(capi), seq_args(capi)
     plain = L.attn_cache_fwd_workspace_size(r(c), r(s), r(fwd_args(capi)))
-    with_w = L.attn_cache_fwd_workspace_size(r(c), r(s), r(fwd_args(capi, weights=FAKE, weights_out=FAKE)))
+    with_w = L.attn_cache_fwd_workspace_size(r(c), r(s), r(fwd_args(capi, weights=FAKE, weights_out=FAKE, weights_stride_b=512,
+                                                                               weights_stride_h=256)))
     assert with_w - plain == 4 * 2 * 4 * 1 * 4 * 64  # 4 * B * Hq * Sq * max_pages * page_size
 
 
