@@ -256,7 +256,7 @@ def test_attention_arguments_of_the_binding():
     with pytest.raises(ValueError, match="strides"):
         go(weights=w, weights_out=torch.zeros(2, 2, 130)[:, :, :128])
     for bad in (torch.zeros(1, 2, 128).expand(2, 2, 128), torch.zeros(2, 1, 128).expand(2, 2, 128),
-                torch.zeros(400).as_strided((2, 2, 128), (200, 100, 1)), torch.zeros(400).as_strided((2, 2, 128), (130, 130, 1))):
+                torch.zeros(500).as_strided((2, 2, 128), (200, 100, 1)), torch.zeros(500).as_strided((2, 2, 128), (130, 130, 1))):
         with pytest.raises(ValueError, match="weights.* must not overlap"):
             go(weights=bad)
     for good in (torch.zeros(2, 2, 128).transpose(0, 1), torch.zeros(600).as_strided((2, 2, 128), (128, 300, 1))):
