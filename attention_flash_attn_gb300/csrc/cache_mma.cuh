@@ -249,7 +249,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
   }
   for (int x = tid; x < C::ROWS * D / 32; x += kThreads) s_nan[x] = 0u;
   if (tid == 0) s_any = 0;
-  __syncwarp();
+  __syncthreads();  // a warp may mark NaNs as soon as its own first slice has come: not before every warp has cleared its part
 
   __shared__ Groups s_groups;
   Cursor cur;
@@ -272,7 +272,6 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
       seq_len(p.c, run.b, &bad);
       if (bad) set_status(p.c.status, kStatusBadPage);
     }
-    __syncthreads();  // s_nan, s_any
   } else if (!cursor_begin(p, &s_groups, cur) || !cursor_next(p, &s_groups, cur, run)) {
     grid_launch_next();
     return;
