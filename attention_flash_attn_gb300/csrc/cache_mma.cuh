@@ -337,9 +337,9 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
       odd_now = __ballot_sync(~0u, odd);
     };
     // Fills ring stage `st` with slice x (ids: its batch).  All lanes call it; lane 0 issues, or, where a
-    // slice spans several pages, a lane for each.
-    auto issue = [&](int x, int st, const int *ids) {
-      const uint32_t bar = bars + 8 * st, dst = ring + st * C::STAGE;
+    // slice spans several pages, a lane for each.  `hold` is 0, known only once the stage's loads have come.
+    auto issue = [&](int x, int st, const int *ids, uint32_t hold) {
+      const uint32_t bar = bars + 8 * st + hold, dst = ring + st * C::STAGE + hold;
       const int pos = key0 + (warp + kWarps * x) * C::SK;
       const int slot = pos & (p.c.page - 1);
       int id = __shfl_sync(~0u, ids[0], x & 31);
@@ -399,7 +399,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
     for (int h = 0; h < C::NH; ++h) id_now[h] = id_nxt[h];
     int filled = dead ? 0 : min(C::DEPTH, n_slices);  // slices asked for
 #pragma unroll 1
-    for (int s = 0; s < filled; ++s) issue(s, stage + s >= C::DEPTH ? stage + s - C::DEPTH : stage + s, id_now);
+    for (int s = 0; s < filled; ++s) issue(s, stage + s >= C::DEPTH ? stage + s - C::DEPTH : stage + s, id_now, 0u);
     fetch_scales();
     if (n_slices <= 0) load_next_ids(0);
 
@@ -500,6 +500,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
         lv[h] = __shfl_sync(~0u, lv_now[h], x & 31);
       }
       const bool partial = ((odd_now >> (x & 31)) & 1u) || pos + C::SK > all_below || pos < all_from;
+      uint32_t come = 0;  // a word of each load of values: see below
       if (!dead) {
         // (Two accumulators where few n-tiles would make the k-steps one long chain.)
         float s[MT][C::SK / 8][4], s2[MT][C::SPLIT ? C::SK / 8 : 1][4];
@@ -691,10 +692,12 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
                 vw[q][1] = u.y;
                 vw[q][C::BLK / 32 - 2] = u.z;
                 vw[q][C::BLK / 32 - 1] = u.w;
+                come |= u.x;
               } else {
                 const uint2 u = lds64(at + swz<C::BLK>(2 * t + (q & 1), g >> 1) + (g & 1) * 8);
                 vw[q][0] = u.x;
                 vw[q][1] = u.y;
+                come |= u.x;
               }
             }
 #pragma unroll
@@ -714,12 +717,16 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
               }
           }
       }
-      __syncwarp();  // every lane has read the stage (and multiplied what it read: the loads have come)
+      // The stage is filled again only once every lane's loads have come: nothing orders a load before a later copy by
+      // TMA into its place but the load's own end (it may be held up behind stores of scores), and the compiler may
+      // move products past the copy.  So the copy's addresses hang on a word of each lane's loads of values (p.splits is
+      // 0 here); those of keys came before the scores that the votes above went by.
       if (x + C::DEPTH < n_slices && !dead) {
         const int y = x + C::DEPTH;
         ++filled;
-        issue(y, stage, (y >> 5) == (x >> 5) ? id_now : id_nxt);
+        issue(y, stage, (y >> 5) == (x >> 5) ? id_now : id_nxt, __reduce_or_sync(~0u, come) & (uint32_t)p.splits);
       }
+      __syncwarp();
       stage = stage + 1 == C::DEPTH ? 0 : stage + 1;
     }
 

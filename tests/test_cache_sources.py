@@ -19,3 +19,16 @@ def test_marks_of_nans_are_cleared_by_all_warps_before_any_warp_begins():
     cleared = s.index("s_nan[x] = 0u")
     parts = s.index("if (p.cluster)", cleared)
     assert "s_any = 0" in s[cleared:parts] and "__syncthreads()" in s[cleared:parts]
+
+
+def test_a_stage_is_refilled_only_behind_its_own_loads():
+    """A load from shared memory may come later than a copy by TMA that was asked for behind it: the copy's addresses have to
+    hang on what each lane loaded from the stage."""
+    s = source("cache_mma.cuh")
+    loop = s[s.index("for (int x = 0; x < n_slices; ++x)"):]
+    refill = re.search(r"issue\(y, stage,[^;]*;", loop)[0]
+    assert re.search(r"__reduce_or_sync\(~0u, come\)", refill)
+    values = re.findall(r"const uint[24] u = lds\w+\(at[^;]*;(.*?)\}", loop[:loop.index(refill)], re.S)
+    assert len(values) == 2 and all("come |= u.x" in v for v in values)
+    issue = re.search(r"auto issue = \[&\]\(([^)]*)\) \{\s*const uint32_t bar = ([^,]*), dst = ([^;]*);", s)
+    assert "hold" in issue[1] and "hold" in issue[2] and "hold" in issue[3]
