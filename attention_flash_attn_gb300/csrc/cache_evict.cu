@@ -43,7 +43,8 @@ __device__ __forceinline__ int warp_prefix(int x, int lane) {
 // passes over shared memory.  Clusters of 16 instead of 8 took half as long again.
 __global__ void __launch_bounds__(kSelThr) cache_select_kernel(const __grid_constant__ EvictParams p, int in_smem) {
   extern __shared__ __align__(16) float s_w[];
-  __shared__ unsigned s_hist[2][kBins], s_group[2][32];
+  __shared__ __align__(16) unsigned s_hist[2][kBins];  // (read in fours)
+  __shared__ unsigned s_group[2][32];
   __shared__ int s_gt[kSelWarps], s_eq[kSelWarps], s_all[2], s_found[2];
   const cg::cluster_group cluster = cg::this_cluster();
   const int rank = cluster.block_rank(), ranks = cluster.num_blocks();

@@ -32,3 +32,19 @@ def test_a_stage_is_refilled_only_behind_its_own_loads():
     assert len(values) == 2 and all("come |= u.x" in v for v in values)
     issue = re.search(r"auto issue = \[&\]\(([^)]*)\) \{\s*const uint32_t bar = ([^,]*), dst = ([^;]*);", s)
     assert "hold" in issue[1] and "hold" in issue[2] and "hold" in issue[3]
+
+
+def test_shared_arrays_read_in_fours_are_declared_aligned():
+    """Arrays of single words in shared memory that are accessed 16 bytes at a time start on 16 bytes by their declaration, not
+    by where the compiler happens to put them."""
+    found = set()
+    for name in sorted(f for f in os.listdir(CSRC) if f.startswith("cache_")):
+        s = source(name)
+        alias = dict(re.findall(r"\*\s*(\w+) = (s_\w+)\[", s))
+        wide = {alias.get(x, x) for x in re.findall(r"reinterpret_cast<(?:const )?(?:uint4|float4|int4) \*>\((\w+)", s)}
+        for align, array in re.findall(r"__shared__ (__align__\(16\) )?(?:unsigned|int|float|uint32_t) ([^;]*);", s):
+            for x in re.findall(r"(\w+)\[", array):
+                if x in wide:
+                    found.add(x)
+                    assert align, (name, x)
+    assert "s_hist" in found
