@@ -363,23 +363,32 @@ __global__ void __launch_bounds__(kThreads) cache_join_kernel(const __grid_const
 
 // weights_out = weights + sum over the rows of 2^(score - LSE): four keys per thread, the rows'
 // scores read as the attention kernel stored them, four rows at a time (loads before sums: bound by
-// the latency of each otherwise), summed in row order.
+// the latency of each otherwise), summed in row order.  A block takes the queries that see any of its keys, which
+// are neighbours; where there are none, nothing is read, and in place nothing is written either.
 __global__ void __launch_bounds__(kThreads) cache_weights_kernel(const __grid_constant__ FwdParams p) {
+  constexpr int kKeys = 4 * kThreads;
   const int b = blockIdx.x / p.c.Hkv, hk = blockIdx.x - b * p.c.Hkv;
   const int len = seq_len(p.c, b);
-  const int j0 = (blockIdx.y * kThreads + threadIdx.x) * 4;
+  const int k0 = blockIdx.y * kKeys, j0 = k0 + threadIdx.x * 4;
+  const int q0 = len - p.Sq;  // position of query 0
+  const int i0 = p.causal ? max(0, k0 - q0) : 0;                                        // the first query that sees one of the block's keys,
+  const int i1 = p.window > 0 ? min(p.Sq, k0 + kKeys - 1 + p.window - q0) : p.Sq;       // and the first behind them
+  const bool any = k0 < len && i0 < i1;
   const size_t at = (size_t)b * p.w_sb + (size_t)hk * p.w_sh + j0;
   float w[4] = {0.f, 0.f, 0.f, 0.f}, sum[4] = {0.f, 0.f, 0.f, 0.f};
+  if (any || p.w_in != p.w_out) {
 #pragma unroll
-  for (int x = 0; x < 4; ++x)
-    if (j0 + x < len) w[x] = p.w_in[at + x];
+    for (int x = 0; x < 4; ++x)
+      if (j0 + x < len) w[x] = p.w_in[at + x];
+  }
   grid_wait();
-  if (j0 >= len) return;
-  const float *row = scores_row(p, b, hk, 0) + j0;
+  if (j0 >= len || (!any && p.w_in == p.w_out)) return;
+  const int r1 = any ? i1 * p.G : 0;
+  const float *row = scores_row(p, b, hk, i0 * p.G) + j0;
   const float *lse = p.LSE + ((size_t)b * p.Hq + hk * p.G) * p.Sq;
-  int query = 0, head = 0;  // of row r0 + i
+  int query = i0, head = 0;  // of row r0 + i
 #pragma unroll 1
-  for (int r0 = 0; r0 < p.R; r0 += 4, row += 4 * p.Lpad) {
+  for (int r0 = i0 * p.G; r0 < r1; r0 += 4, row += 4 * p.Lpad) {
     // Scores are stored for the keys that some row of the tile sees (a superset of what a row sees); the others, and
     // the last row's in place of those past it, are loaded too, unconditionally so that all loads go out at once (behind
     // conditions each waited for the one before: 86 sequences of 135 keys, 16 heads, 15 rows, 20 us for this pass
@@ -390,10 +399,10 @@ __global__ void __launch_bounds__(kThreads) cache_weights_kernel(const __grid_co
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       lse2[i] = lse[(size_t)head * p.Sq + query];
-      s[i] = *reinterpret_cast<const float4 *>(row + (min(r0 + i, p.R - 1) - r0) * p.Lpad);
+      s[i] = *reinterpret_cast<const float4 *>(row + (min(r0 + i, r1 - 1) - r0) * p.Lpad);
       see[i] = row_sees(p, len, query);
-      if (r0 + i >= p.R) see[i] = make_int2(0, 0);
-      if (r0 + i < p.R - 1 && ++head == p.G) {
+      if (r0 + i >= r1) see[i] = make_int2(0, 0);
+      if (r0 + i < r1 - 1 && ++head == p.G) {
         head = 0;
         ++query;
       }
