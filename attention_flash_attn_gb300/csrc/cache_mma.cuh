@@ -15,7 +15,9 @@
 //   - TMA's swizzle makes both 16-byte access patterns free of bank conflicts.
 //   - Q is scaled per row by a power of two into fp16's range: exact for elements within 2^-31 of the
 //     row's largest.
-//   - P is rounded to fp16 (half a step: 2^-11 of each probability, eight times finer than the bf16 result).
+//   - P is rounded to fp16 (half a step: 2^-11 of each probability, eight times finer than the bf16 result), times
+//     2^14, so that the many small probabilities beside a large one keep their bits down to 2^-28 of it (held
+//     as they are, from 2^-14 on they did not, and below 2^-25 they were 0, while the sum counted them).
 //   - float queries take the same way in two terms each: q = hi + lo in fp16 (22 bits), p 2^14 = hi + lo, both
 //     terms multiplied into the same accumulators.  Twice the MMAs; the FFMA kernel took 39 us where this
 //     takes 16 (9 ragged rows up to 9001 keys, one kv head).
@@ -35,12 +37,12 @@ using namespace attn::tc;
 
 constexpr int kWarps = kThreads / 32;
 constexpr float kZeroLog = kMinScaleExp - 1;
+constexpr float kPShift = 14;  // probabilities (at most 1) are held times 2^14: fp16 is normal down to 2^-28 of the row's largest
 
 template <typename T, int D_, int MT_>
 struct Cfg {
   static constexpr int D = D_, MT = MT_;
   static constexpr int TERMS = sizeof(T) == 4 ? 2 : 1;  // fp16 terms of a query element and of a probability
-  static constexpr int PSHIFT = sizeof(T) == 4 ? 14 : 0;  // probabilities are held times 2^PSHIFT: two terms without subnormals
   static constexpr int SK = D == 256 ? 16 : D == 128 ? 32 : 64;  // keys of a slice: 8 KB of codes
   static constexpr int NH = SK / 16;                   // groups of 16 keys: each lies in one page
   static constexpr int BLK = D < 128 ? D : 128;        // columns of one TMA box row
@@ -662,7 +664,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              const float ref = lv[h] - (m[mt][y] == -CUDART_INF_F ? 0.f : m[mt][y]) + (float)C::PSHIFT;
+              const float ref = lv[h] - (m[mt][y] == -CUDART_INF_F ? 0.f : m[mt][y]) + kPShift;
               float e[4];
 #pragma unroll
               for (int q = 0; q < 4; ++q) e[q] = ex2(fmaf(f[mt][y][h], s[mt][2 * h + (q >> 1)][2 * y + (q & 1)], ref));
@@ -748,7 +750,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
           float v = l[mt][y];
           v += __shfl_xor_sync(~0u, v, 1);
           v += __shfl_xor_sync(~0u, v, 2);
-          if (t == 0) s_ml[warp * C::ROWS + r] = make_float2(m[mt][y] - (float)C::PSHIFT, dead ? CUDART_NAN_F : v);
+          if (t == 0) s_ml[warp * C::ROWS + r] = make_float2(m[mt][y] - kPShift, dead ? CUDART_NAN_F : v);
 #pragma unroll
           for (int e = 0; e < 2; ++e)
 #pragma unroll

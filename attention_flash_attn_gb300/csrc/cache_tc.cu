@@ -9,7 +9,7 @@
 //                 small ring;
 //   warp 1        MMA issuer: S_j = Q K_j^T into one of two TMEM buffers, O += P_{j-1} V_{j-1} with P in TMEM;
 //   warps 2..9    softmax: a row is a TMEM lane, the two warps of a lane quarter split its keys (as in the
-//                 dense forward); O is rescaled only when a row's reference grew by more than 2^8;
+//                 dense forward); O is rescaled only when a row's reference grew by more than 2^4;
 //   warps 10..13  converters: the queries once, scaled per row by a power of two into fp16, then every tile's
 //                 codes widened to fp16 (exactly) into the 128-byte-swizzled operand layout.
 // Scales never touch the operands: a key's scale multiplies its scores, a value's enters the exponent of the
@@ -33,7 +33,9 @@ using namespace attn::tc;
 
 constexpr int kTcThreads = 448;
 constexpr int kBM = 128, kBN = 128, kHC = kBN / 2;
-constexpr float kLazy = 8.f;  // growth of a row's reference (log2) that P may reach before O is rescaled
+// Growth of a row's reference (log2) that P may reach before O is rescaled, and what P is held times (log2): at most
+// 2^15 in fp16, and normal down to 2^-25 of the row's largest.  (Rescaling from 2^8 on took the same time.)
+constexpr float kLazy = 4.f, kPShift = 11.f;
 constexpr float kZeroLog = kMinScaleExp - 1;
 constexpr int kFailed = 0x7fffdead;  // a partner's row maximum that says that a wait gave up (no NaN that arithmetic gives)
 
@@ -521,7 +523,7 @@ cache_tc_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUt
         uint32_t pk[16];
 #pragma unroll
         for (int g = 2 * q; g < 2 * q + 2; ++g) {
-          const uint64_t f2 = f2_splat(f[g]), ref2 = f2_splat(lv[g] - mr);
+          const uint64_t f2 = f2_splat(f[g]), ref2 = f2_splat(lv[g] - mr + kPShift);
           uint64_t sum = 0;  // (two floats)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -570,17 +572,18 @@ cache_tc_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUt
   grid_launch_next();
   if (warp >= 2 && warp < 10) {
     const int wq = warp & 3, half = (warp - 2) >> 2, r = wq * 32 + lane;
+    const float M = m_ref - kPShift;  // what O and the sum are relative to
     if (wq * 32 < rows) {
       const float L = xbuf[2 * kBM + r] + xbuf[5 * kBM + r];
       const uint32_t lane_addr = tmem + ((uint32_t)(wq * 32) << 16);
       const bool row_ok = r < rows, nans = misc[1] != 0, whole = p.splits == 1;
-      const RowEnd e = row_end(p, hk * p.G + (r0 + min(r, rows - 1)) % p.G, m_ref, L);
+      const RowEnd e = row_end(p, hk * p.G + (r0 + min(r, rows - 1)) % p.G, M, L);
       const size_t part = (size_t)blockIdx.x * kBM + r;
       if (row_ok && half == 0) {
         if (whole) p.LSE[lse_at(p, b, hk, r0 + r)] = e.lse;
-        else p.ml_part[part] = make_float2(m_ref, L);
+        else p.ml_part[part] = make_float2(M, L);
       }
-      const bool none = n == 0 || m_ref == -CUDART_INF_F;
+      const bool none = n == 0 || M == -CUDART_INF_F;
 #pragma unroll 1
       for (int c = half * (D / 64); c < (half + 1) * (D / 64); ++c) {
         uint32_t o[32];

@@ -111,7 +111,9 @@ int attn_cache_append(const attn_cache *c, const attn_cache_seqs *s, const attn_
  * the queries scaled per row by a power of two into fp16: bf16 queries exactly (elements within
  * 2^-31 of the row's largest) with probabilities rounded to fp16, float queries and their
  * probabilities in two fp16 terms (22 bits).  Many bf16 rows per kv head at head dims up to
- * 128 take tcgen05 products.  Larger head dims run on fp32 FFMA kernels.  Long key ranges are split
+ * 128 take tcgen05 products.  What is rounded is a probability times its value's scale: half a step
+ * is 2^-11 of it down to 2^-28 (tcgen05: 2^-25) of the row's largest such product, and below 2^-39
+ * (2^-36) of that largest one.  Larger head dims run on fp32 FFMA kernels.  Long key ranges are split
  * over CTAs and joined in a fixed order; how, depends on the shapes and the lengths alone.
  */
 typedef struct {
