@@ -502,7 +502,6 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
         lv[h] = __shfl_sync(~0u, lv_now[h], x & 31);
       }
       const bool partial = ((odd_now >> (x & 31)) & 1u) || pos + C::SK > all_below || pos < all_from;
-      uint32_t come = 0;  // a word of each load of values: see below
       if (!dead) {
         // (Two accumulators where few n-tiles would make the k-steps one long chain.)
         float s[MT][C::SK / 8][4], s2[MT][C::SPLIT ? C::SK / 8 : 1][4];
@@ -677,6 +676,17 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
               }
             }
         }
+        // The stage is filled again as soon as every lane's loads of it have come, and not before: nothing orders a load
+        // before a later copy by TMA into its place but the load's own end (it may be held up behind stores of scores), and
+        // the compiler may move products past the copy.  So the copy's addresses hang on a vote over a word of each load
+        // of values (p.splits is 0 here); those of keys came before the scores that the votes above went by.
+        uint32_t come = 0;
+        auto refill = [&]() {
+          const int y = x + C::DEPTH;
+          if (y >= n_slices) return;
+          ++filled;
+          issue(y, stage, (y >> 5) == (x >> 5) ? id_now : id_nxt, __any_sync(~0u, come == 0x9e3779b9u) ? (uint32_t)p.splits : 0u);
+        };
         // O += P V: lane t has keys 2t, 2t + 1, 2t + 8, 2t + 9 of each 16 as the B operand's rows, and
         // BLK / 8 neighbouring columns, one for each n-tile.
 #pragma unroll
@@ -702,6 +712,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
                 come |= u.x;
               }
             }
+            if (j == C::NB - 1 && h == C::NH - 1) refill();
 #pragma unroll
             for (int w = 0; w < C::BLK / 32; ++w)
 #pragma unroll
@@ -718,15 +729,6 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
                     for (int q = 0; q < C::TERMS; ++q) mma_f16(o[mt][j * (C::BLK / 8) + 4 * w + 2 * z + e], pf[q][mt][h], b0[e], b1[e]);
               }
           }
-      }
-      // The stage is filled again only once every lane's loads have come: nothing orders a load before a later copy by
-      // TMA into its place but the load's own end (it may be held up behind stores of scores), and the compiler may
-      // move products past the copy.  So the copy's addresses hang on a word of each lane's loads of values (p.splits is
-      // 0 here); those of keys came before the scores that the votes above went by.
-      if (x + C::DEPTH < n_slices && !dead) {
-        const int y = x + C::DEPTH;
-        ++filled;
-        issue(y, stage, (y >> 5) == (x >> 5) ? id_now : id_nxt, __reduce_or_sync(~0u, come) & (uint32_t)p.splits);
       }
       __syncwarp();
       stage = stage + 1 == C::DEPTH ? 0 : stage + 1;

@@ -27,9 +27,11 @@ def test_a_stage_is_refilled_only_behind_its_own_loads():
     s = source("cache_mma.cuh")
     loop = s[s.index("for (int x = 0; x < n_slices; ++x)"):]
     refill = re.search(r"issue\(y, stage,[^;]*;", loop)[0]
-    assert re.search(r"__reduce_or_sync\(~0u, come\)", refill)
-    values = re.findall(r"const uint[24] u = lds\w+\(at[^;]*;(.*?)\}", loop[:loop.index(refill)], re.S)
+    assert re.search(r"__any_sync\(~0u, come\b", refill) and "p.splits" in refill
+    assert loop.count("issue(") == 1
+    values = re.findall(r"const uint[24] u = lds\w+\(at[^;]*;(.*?)\}", loop, re.S)
     assert len(values) == 2 and all("come |= u.x" in v for v in values)
+    assert loop.index("= lds64(at") < loop.index("h == C::NH - 1) refill();") < loop.index("mma_f16(o[")
     issue = re.search(r"auto issue = \[&\]\(([^)]*)\) \{\s*const uint32_t bar = ([^,]*), dst = ([^;]*);", s)
     assert "hold" in issue[1] and "hold" in issue[2] and "hold" in issue[3]
 
