@@ -95,11 +95,11 @@ __global__ void __launch_bounds__(kThreads) cache_fwd_simt_kernel(const __grid_c
       float s[kRows];
 #pragma unroll
       for (int r = 0; r < kRows; ++r) s[r] = 0.f;
-      float ks = 0.f, lv = 0.f, inv = 1.f;
+      float ks = 0.f, lv = 0.f;
       bool zero = true;
       if (page >= 0) {
         ks = p.c.k_scale[(size_t)page * p.c.Hkv + run.hk] * p.scale;
-        lv = scale_log2(p.c.v_scale[(size_t)page * p.c.Hkv + run.hk], &inv, &zero);
+        lv = scale_log2(p.c.v_scale[(size_t)page * p.c.Hkv + run.hk], &zero);
         const uint4 *krow = reinterpret_cast<const uint4 *>(p.c.k + row_at(p.c, page, run.hk, slot));
         for (int d = 0; d < D; d += 16) {
           const uint4 w = krow[d >> 4];
@@ -127,13 +127,15 @@ __global__ void __launch_bounds__(kThreads) cache_fwd_simt_kernel(const __grid_c
         if (p.scores && r < rows) scores_row(p, run.b, run.hk, r0 + r)[pos] = t2;
         const float e = t2 + lv;
         const float mn = max_nan(m[r], warp_max(e));
-        float pr = 0.f, alpha = 1.f;
+        float pr = 0.f, half = 1.f, one = 0.f;
         if (mn != -CUDART_INF_F) {
           pr = vis ? exp2f(e - mn) : 0.f;
-          alpha = exp2f(m[r] - mn);
+          one = vis ? exp2f(t2 - mn + kFarUp) : 0.f;  // (by an exponential of its own whatever the scale: see cache_work.cuh)
+          half = exp2f(0.5f * (m[r] - mn));
         }
+        const float alpha = half * half;
         m[r] = mn;
-        l[r] = l[r] * alpha + pr * inv;
+        l[r] = rescaled(l[r], half) + one * 0x1p-40f;
         if (alpha != 1.f) {
 #pragma unroll
           for (int c = 0; c < NC; ++c)
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(kThreads) cache_fwd_simt_kernel(const __grid_c
       for (int w = 0; w < kWarps; ++w) M = max_nan(M, s_ml[w * kRows + r].x);
       for (int w = 0; w < kWarps; ++w) {
         const float2 ml = s_ml[w * kRows + r];
-        if (ml.x != -CUDART_INF_F) L += ml.y * exp2f(ml.x - M);
+        if (ml.x != -CUDART_INF_F) L += rescaled(ml.y, exp2f(0.5f * (ml.x - M)));
       }
       float scale = 1.f;
       if (whole) {
@@ -310,10 +312,10 @@ __global__ void __launch_bounds__(kThreads) cache_join_kernel(const __grid_const
     float top = M;
 #pragma unroll
     for (int i = 0; i < 4; ++i) top = max_nan(top, ml[i].x);
-    L *= top == -CUDART_INF_F ? 1.f : exp2f(M - top);
+    L = rescaled(L, top == -CUDART_INF_F ? 1.f : exp2f(0.5f * (M - top)));
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (ml[i].x != -CUDART_INF_F) L += ml[i].y * exp2f(ml[i].x - top);
+      if (ml[i].x != -CUDART_INF_F) L += rescaled(ml[i].y, exp2f(0.5f * (ml[i].x - top)));
     M = top;
   }
   if (PER_ROW > 1) {  // the warps' parts of the row
@@ -325,7 +327,7 @@ __global__ void __launch_bounds__(kThreads) cache_join_kernel(const __grid_const
     for (int w = 0; w < PER_ROW; ++w) M = max_nan(M, s_ml[w].x);
 #pragma unroll
     for (int w = 0; w < PER_ROW; ++w)
-      if (s_ml[w].x != -CUDART_INF_F) L += s_ml[w].y * exp2f(s_ml[w].x - M);
+      if (s_ml[w].x != -CUDART_INF_F) L += rescaled(s_ml[w].y, exp2f(0.5f * (s_ml[w].x - M)));
     const float f = mine == -CUDART_INF_F ? 0.f : exp2f(mine - M);
 #pragma unroll
     for (int x = 0; x < 4; ++x) {

@@ -226,13 +226,25 @@ __device__ __forceinline__ void scrub_values(const FwdParams &p, uint8_t *sv, in
   __syncwarp();
 }
 
+// recount for rows r0 .. r0 + rows - 1 of (kv head, sequence) pair `hb`, whose references and sums lie in ml.  Called by a warp.
+template <typename T, int KIND>
+__device__ __noinline__ void recount_rows(const FwdParams &p, int hb, int r0, int len, Keys keys, float2 *ml, int rows) {
+  const int hk = hb / p.c.B, b = hb - hk * p.c.B;
+  if (!far_apart(p, b, hk, keys)) return;
+#pragma unroll 1
+  for (int r = 0; r < rows; ++r) {
+    const float sum = recount<T, KIND>(p, b, hk, r0 + r, len, keys, ml[r].x);
+    if ((threadIdx.x & 31) == 0) ml[r].y = sum;
+  }
+}
+
 template <typename T, int KIND, int D, int MT>
 __global__ void __launch_bounds__(kThreads, (Cfg<T, D, MT>::CTAS))
 cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg<T, D, MT>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int s_any;
+  __shared__ int s_any, s_large;  // s_large: a value scale so large that others may be too far below it (see cache_work.cuh)
   const uint32_t raw = smem_u32(smem_raw), ring0 = (raw + 1023u) & ~1023u;
   uint8_t *base = smem_raw + (ring0 - raw);
   uint4 *s_q = reinterpret_cast<uint4 *>(base + C::RING);                                      // [TERMS][MT][KS][32]
@@ -250,7 +262,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
     tma_prefetch_desc(&vmap);
   }
   for (int x = tid; x < C::ROWS * D / 32; x += kThreads) s_nan[x] = 0u;
-  if (tid == 0) s_any = 0;
+  if (tid == 0) s_any = 0, s_large = 0;
   __syncthreads();  // a warp may mark NaNs as soon as its own first slice has come: not before every warp has cleared its part
 
   __shared__ Groups s_groups;
@@ -335,6 +347,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
       for (int h = 0; h < C::NH; ++h) {
         odd |= !(lv_now[h] >= kMinScale);
         lv_now[h] = lv_now[h] >= kMinScale ? log2f(lv_now[h]) : kZeroLog;
+        if (lv_now[h] > kFarTop) s_large = 1;
       }
       odd_now = __ballot_sync(~0u, odd);
     };
@@ -764,9 +777,12 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
             }
         }
     }
+    __syncwarp();
+    if (s_large && !dead)  // (set by this warp or another: the warp's own keys decide)
+      recount_rows<T, KIND>(p, run.hk * p.c.B + run.b, r0, run.range.len, {key0 + warp * C::SK, C::SK, kWarps * C::SK, key1}, s_ml + warp * C::ROWS, rows);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring's next fill comes by TMA
     __syncthreads();
-    const bool one_of = p.cluster > 1, whole = !one_of && run.cnt == run.n, nans = s_any != 0;
+    const bool one_of = p.cluster > 1, whole = !one_of && run.cnt == run.n, nans = s_any != 0, large = s_large != 0;
 #pragma unroll 1
     for (int x = tid; x < rows * (D / 4); x += kThreads) {
       const int r = x / (D / 4), d = (x % (D / 4)) * 4;
@@ -784,7 +800,7 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
         if (ml[w].x == -CUDART_INF_F) continue;
         const float f = ex2(ml[w].x - M);
         const float4 u = *reinterpret_cast<const float4 *>(base + w * (C::DEPTH * C::STAGE) + o_at(r, d) * 4);
-        L += f * ml[w].y;
+        L += large ? rescaled(ml[w].y, ex2(0.5f * (ml[w].x - M))) : f * ml[w].y;
         v.x += f * u.x;
         v.y += f * u.y;
         v.z += f * u.z;
@@ -825,9 +841,9 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
           const float4 u = dsmem_f4(v_at, k);
           const float top = max_nan(M, ml.x);
           if (top == -CUDART_INF_F) continue;
-          const float a = ex2(M - top), f = ex2(ml.x - top);
+          const float ha = ex2(0.5f * (M - top)), hf = ex2(0.5f * (ml.x - top)), a = ha * ha, f = hf * hf;
           M = top;
-          L = L * a + f * ml.y;
+          L = rescaled(L, ha) + rescaled(ml.y, hf);
           v.x = v.x * a + f * u.x;
           v.y = v.y * a + f * u.y;
           v.z = v.z * a + f * u.z;
@@ -842,9 +858,9 @@ cache_fwd_mma_kernel(const __grid_constant__ FwdParams p, const __grid_constant_
     }
     if (p.cluster) return;
     __syncthreads();  // the ring, s_ml and s_nan are free for the next run
-    if (nans) {
+    if (nans || large) {
       for (int x = tid; x < C::ROWS * D / 32; x += kThreads) s_nan[x] = 0u;
-      if (tid == 0) s_any = 0;
+      if (tid == 0) s_any = s_large = 0;
       __syncthreads();
     }
   } while (cursor_next(p, &s_groups, cur, run));

@@ -145,7 +145,7 @@ cache_tc_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUt
   float *xbuf = reinterpret_cast<float *>(smem + C::OFF_X), *s_qm = reinterpret_cast<float *>(smem + C::OFF_QM);
   uint32_t *s_nan = reinterpret_cast<uint32_t *>(smem + C::OFF_NAN);
   Info *info = reinterpret_cast<Info *>(smem + C::OFF_INFO);
-  int *misc = reinterpret_cast<int *>(smem + C::OFF_MISC);  // 0: TMEM address, 1: any NaN marked
+  int *misc = reinterpret_cast<int *>(smem + C::OFF_MISC);  // 0: TMEM address, 1: any NaN marked, 2: any large scale
 
   // This CTA's tile and keys.
   const int item = blockIdx.x / p.splits, sp = blockIdx.x - item * p.splits;
@@ -189,7 +189,7 @@ cache_tc_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUt
       mbar_init(i_empty(x), 8);
     }
     fence_barrier_init();
-    misc[1] = 0;
+    misc[1] = misc[2] = 0;
     if (sp == 0 && hk == 0 && rt == 0) {
       bool bad;
       seq_len(p.c, b, &bad);
@@ -261,7 +261,9 @@ cache_tc_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUt
           const unsigned gone = __ballot_sync(~0u, id < 0) >> (8 * sub), zeros = __ballot_sync(~0u, zero) >> (8 * sub);
           if (mine) {
             info[sub].ks[grp] = ks;
-            info[sub].lv[grp] = zero ? kZeroLog : log2f(vs);
+            const float lv = zero ? kZeroLog : log2f(vs);
+            info[sub].lv[grp] = lv;
+            if (lv > kFarTop) misc[2] = 1;
             if (grp == 0) {
               info[sub].gone = gone & 255u;
               info[sub].zero = zeros & 255u;
@@ -562,6 +564,18 @@ cache_tc_kernel(const __grid_constant__ FwdParams p, const __grid_constant__ CUt
     }
     if (active && ok && n > 0) ok = mbar_wait_warp(o_done, (n - 1) & 1, p.c.status);
     tc_fence_after();
+    // A scale so large that others may be too far below it (the records of all tiles were waited for): see
+    // cache_work.cuh.  Each half counts 16 of the quarter's rows, and nothing for the others.
+    const Keys keys = {key0, 512, 512, key1};
+    if (active && n > 0 && misc[2] && __all_sync(~0u, ok) && far_apart(p, b, hk, keys)) {
+      l = 0.f;
+#pragma unroll 1
+      for (int z = half * 16; z < half * 16 + 16 && wq * 32 + z < rows; ++z) {
+        const float M = __shfl_sync(~0u, m_ref, z);
+        const float sum = recount<__nv_bfloat16, KIND>(p, b, hk, r0 + wq * 32 + z, range.len, keys, M - kPShift);
+        if (lane == z) l = sum;
+      }
+    }
     xbuf[(half * 3 + 2) * kBM + r] = ok ? l : CUDART_NAN_F;
   }
 

@@ -11,6 +11,11 @@
 //   O' = sum_j 2^(t_j + lv_j - M) code_j,      l = sum_j 2^(t_j + lv_j - M) 2^-lv_j,
 // so the scale costs nothing per element of V and the 2^(..) fed to the MMA stay within (0, 1]
 // whatever the pages' scales; O = O' / l and LSE = ln2 (M + log2 l).
+// Beside a value scale 2^126 times as large, a key's 2^(t + lv - M) is 0 in float where its 2^(t - M) may be all of the
+// sum (and its value nothing of the output), and M moves by more than float's exponents between terms of one size.
+// Where the scales of a run's keys lie more than kFar apart, its rows' sums are therefore formed once more at its
+// end, key by key, by exponentials of their own (recount); nearer ones lose 2^-46 of the sum for each key, or less.
+// Parts are joined with their sums rescaled in two steps.
 #pragma once
 
 #include "cache_common.cuh"
@@ -170,13 +175,87 @@ __device__ __forceinline__ int2 row_sees(const FwdParams &p, int len, int i) {
 }
 __device__ __forceinline__ bool within(int2 see, int key) { return key >= see.x && key < see.y; }
 
-// The logarithm (base 2) of a page's value scale, and its inverse; scales below 2^-60 count as 0.
-__device__ __forceinline__ float scale_log2(float vs, float *inv, bool *zero) {
+// The logarithm (base 2) of a page's value scale; scales below 2^-60 count as 0.
+__device__ __forceinline__ float scale_log2(float vs, bool *zero) {
   *zero = !(vs >= kMinScale);
-  const float s = *zero ? kMinScale : vs;
-  const float lv = log2f(s);
-  *inv = exp2f(-lv);
-  return lv;
+  return log2f(*zero ? kMinScale : vs);
+}
+
+constexpr float kFar = 80.f;
+constexpr float kFarTop = kMinScaleExp - 1 + kFar;  // with no lv above it (2^19), none lie further apart
+constexpr float kFarUp = 40.f;  // what recounted terms are held times (log2): see recount
+
+// l * 2^(2 h), in two steps (`half`: 2^h).
+__device__ __forceinline__ float rescaled(float l, float half) { return l * half * half; }
+
+// Elements x .. x + 3 of a row of queries.
+__device__ __forceinline__ float4 query4(const float *q) { return *reinterpret_cast<const float4 *>(q); }
+__device__ __forceinline__ float4 query4(const __nv_bfloat16 *q) {
+  const uint2 u = *reinterpret_cast<const uint2 *>(q);
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
+
+// The keys of a run that one warp has: `block` keys from `first` on, and from every `stride` keys further on, below `end`.
+struct Keys {
+  int first, block, stride, end;
+};
+
+// Whether the value scales of these keys lie more than kFar apart (log2).  Called by a warp.
+static __device__ __noinline__ bool far_apart(const FwdParams &p, int b, int hk, Keys k) {
+  float lo = CUDART_INF_F, hi = -CUDART_INF_F;
+  const int lane = threadIdx.x & 31;
+  for (int base = k.first; base < k.end; base += k.stride)
+    for (int pos = base + 16 * lane; pos < min(k.end, base + k.block); pos += 512) {
+      const int page = page_of(p.c, b, pos);
+      if (page < 0) continue;
+      bool zero;
+      const float lv = scale_log2(p.c.v_scale[(size_t)page * p.c.Hkv + hk], &zero);
+      lo = fminf(lo, lv);
+      hi = fmaxf(hi, lv);
+    }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    lo = fminf(lo, __shfl_xor_sync(~0u, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(~0u, hi, o));
+  }
+  return hi - lo > kFar;
+}
+
+// The sum over these keys of row r's 2^(t - M), in fp32 throughout: a key to a lane, the query broadcast.  Called by a
+// warp, every lane gets the sum.  t - M <= 15 - lv <= 76 (M may lie 15 below the largest t + lv) does not overflow with
+// kFarUp; what underflows is 2^-44 of the sum or less for each key (the sum is 2^-122 or more, as the largest scale is 2^122).
+template <typename T, int KIND>
+__device__ __noinline__ float recount(const FwdParams &p, int b, int hk, int r, int len, Keys k, float M) {
+  if (M == -CUDART_INF_F) return 0.f;
+  const int lane = threadIdx.x & 31, i = query_of(p, r), h = hk * p.G + (r - i * p.G);
+  const T *q = static_cast<const T *>(p.q) + b * p.q_sb + i * p.q_ss + h * p.q_sh;
+  const int2 see = row_sees(p, len, i);
+  float sum = 0.f;
+  for (int base = k.first; base < k.end; base += k.stride)
+    for (int pos = base + lane; pos < min(k.end, base + k.block); pos += 32) {
+      const int page = within(see, pos) ? page_of(p.c, b, pos) : -1;
+      if (page < 0) continue;
+      const uint4 *row = reinterpret_cast<const uint4 *>(p.c.k + row_at(p.c, page, hk, pos & (p.c.page - 1)));
+      float s = 0.f;
+#pragma unroll 1
+      for (int d = 0; d < p.c.D; d += 16) {
+        const uint4 w = row[d / 16];
+        const unsigned words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          float x[4];
+          decode4<KIND>(words[y], x);
+          const float4 v = query4(q + d + 4 * y);
+          s = fmaf(v.x, x[0], fmaf(v.y, x[1], fmaf(v.z, x[2], fmaf(v.w, x[3], s))));
+        }
+      }
+      s *= p.c.k_scale[(size_t)page * p.c.Hkv + hk] * p.scale;
+      if (p.cap > 0.f) s = p.cap * tanhf(s * p.inv_cap);
+      sum += exp2f(s * kLog2e - M + kFarUp);
+    }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  return sum * exp2f(-kFarUp);
 }
 
 // A row's final factors from its reference M and sum l: O = O' * scale.  The extra softmax column

@@ -93,3 +93,69 @@ def test_a_page_of_a_large_scale_and_no_values(dtype, D, Hq, kind):
     vs[c.table[0, 3].long()] = 2.0 ** 18 * vs[c.table[0, 0].long()]
     put(c, v=v, vs=vs)
     check(c, *c.run(), path=path_of(c))
+
+
+# Scales of ten pages of 64 tokens, and what their keys' scales are multiplied by: equal logits, and logits that make up for
+# the values' scales.  2^-60 is what append writes for zeros.
+FAR = [([67, -60], [1, 1]), ([-60, 67], [1, 1]), ([100, -60, 0, -60, 90, -3, -60, 100, 20, -45], [1] * 10),
+       ([-60, -60, 40, 100, -60, 100, -60, -20, 0, 60], [30, 1, 1, 1, 8, 1, 40, 4, 1, 1])]
+
+
+@pytest.mark.parametrize("kind", [E4M3, INT8])
+@pytest.mark.parametrize("dtype,D,Hq", FORMS)
+@pytest.mark.parametrize("powers,louder", FAR)
+@pytest.mark.parametrize("sink", [False, True])
+def test_pages_whose_scales_are_further_apart_than_floats_exponents(dtype, D, Hq, kind, powers, louder, sink):
+    c = Case([64 * len(powers) - 3], Hq=Hq, Hkv=2, D=D, kind=kind, dtype=dtype, spread=0.0, extra_cols=0)
+    ids = c.table[0].long()
+    vs, ks = c.vs.clone(), c.ks.clone()
+    vs[ids] = torch.tensor([2.0 ** x for x in powers])[:, None]
+    ks[ids] *= torch.tensor([float(x) for x in louder])[:, None]
+    put(c, vs=vs, ks=ks)
+    w = c.cuda["w"]
+    O, LSE = c.run(sink=c.cuda["sink"] if sink else None, weights=w)
+    check(c, O, LSE, w, path=path_of(c), sink=sink)
+    O2, LSE2 = c.run(sink=c.cuda["sink"] if sink else None)
+    assert torch.equal(O, O2) and torch.equal(LSE, LSE2)
+
+
+@pytest.mark.parametrize("dtype,D,Hq,Hkv,lengths", [(BF16, 128, 32, 8, [20000, 333]), (BF16, 64, 8, 2, [70000]), (BF16, 256, 8, 2, [9001, 5000]),
+                                                    (F32, 128, 8, 2, [30000]), (BF16, 128, 160, 2, [5000, 2000]), (BF16, 320, 8, 2, [9000]),
+                                                    (BF16, 64, 520, 1, [20000])])
+def test_joined_parts_whose_scales_are_far_apart(dtype, D, Hq, Hkv, lengths):
+    """Runs of pages of one scale each, so that the parts that a row is split into differ by it."""
+    c = Case(lengths, Hq=Hq, Hkv=Hkv, D=D, dtype=dtype, spread=0.0, extra_cols=0)
+    vs = c.vs.clone()
+    for b, n in enumerate(lengths):
+        need = -(-n // 64)
+        for x in range(need):
+            vs[c.table[b, x].long()] = 2.0 ** (-60, 100, 0, 67, -60)[5 * x // need]
+    put(c, vs=vs)
+    w = c.cuda["w"]
+    O, LSE = c.run(weights=w)
+    check(c, O, LSE, w, path=path_of(c))
+
+
+def test_zeros_next_to_large_values_as_append_writes_them():
+    """A page of zero values (scale 2^-60) and one of values around 2^75."""
+    m = fa()
+    cache = m.AttnCache.empty(2, 64, 1, 64)
+    g = torch.Generator().manual_seed(4)
+    k, v = (torch.randn((1, 128, 1, 64), generator=g) for _ in range(2))
+    v[:, :64] = 0.0
+    v[:, 64:] *= 2.0 ** 75
+    table = torch.tensor([[1, 0]], dtype=torch.int32).cuda()
+    n = m.attn_cache_append(cache, k.cuda(), v.cuda(), table, torch.zeros(1, dtype=torch.int32, device="cuda"))
+    assert float(cache.v_scale[1, 0]) == 2.0 ** -60 and float(cache.v_scale[0, 0]) > 2.0 ** 66
+    w = torch.zeros((1, 1, 128), device="cuda")
+    for dtype in (BF16, F32):
+        w.zero_()
+        q = torch.randn((1, 1, 4, 64), generator=g).to(dtype)
+        O, LSE = m.attn_cache_fwd(q.cuda(), cache, table, n, weights=w)
+        kk, vv = (ref.gather(ref.values(x.cpu(), s.cpu()), table[0].cpu(), 128, 64) for x, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
+        o, lse, ww, pv, mag = ref.attend(q[0].double(), kk, vv)
+        _, rel = ref.bounds(64, 128, mag, 0.0, dtype == BF16)
+        eps = torch.finfo(dtype).eps / 2
+        assert ((O[0].cpu().double() - o).abs() <= eps * o.abs() + (1 + eps) * (rel + 2.0 ** -24) * pv).all()
+        assert ((LSE[0].cpu().double() - lse).abs() <= rel + 4 * 2.0 ** -24 * lse.abs()).all()
+        assert ((w[0].cpu().double() - ww).abs() <= (2 * rel + 2.0 ** -20) * ww).all()
