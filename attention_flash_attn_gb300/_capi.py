@@ -113,6 +113,7 @@ class AttnCacheEvictArgs(ctypes.Structure):
         ("weights", ctypes.c_void_p), ("weights_stride_b", ctypes.c_int64), ("weights_stride_h", ctypes.c_int64),
         ("table_out", ctypes.c_void_p), ("table_out_stride", ctypes.c_int64),
         ("kept", ctypes.c_void_p), ("lengths_out", ctypes.c_void_p), ("weights_out", ctypes.c_void_p),
+        ("weights_out_stride_b", ctypes.c_int64), ("weights_out_stride_h", ctypes.c_int64),
     ]
 
 

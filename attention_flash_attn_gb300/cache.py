@@ -118,7 +118,10 @@ def attn_cache_evict(cache: AttnCache, table, lengths, weights, table_out, *, ke
     ties keep the lower position), gathered in order into the pages that table_out [B, >= ceil(keep /
     page_size)] lists.  No page of table_out may be one that the call still reads.  Returns (kept
     [B, Hkv, keep] int32, -1 past the last; new lengths [B] int32; their weights [B, Hkv, keep], 0 past the
-    last): table_out and the latter two are the sequences from here on."""
+    last).  table_out and the new lengths are the sequences from here on; positions, and with them
+    windows, count the tokens that are left.  To go on with accumulated weights, give ``weights_out`` rows
+    of table_out's width ([B, Hkv, >= table_out.shape[1] * page_size] float32, not overlapping weights nor between its rows): it is
+    written up to ``keep``, returned, and what the next append and attention take."""
     return _calls().evict(cache._addr, cache.k, table, lengths, weights, table_out, keep, recent, first, kept, weights_out)
 
 

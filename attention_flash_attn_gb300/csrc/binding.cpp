@@ -331,7 +331,9 @@ PyObject *evict(PyObject *const *a, Py_ssize_t n) {
   page_table(where, "table_out", to, B, ((int64_t)g.keep + c.c->page_size - 1) / c.c->page_size, c);
   const int64_t shape[3] = {B, c.c->Hkv, g.keep};
   const at::Tensor kept = output(where, "kept", a[9], shape, at::kInt, c);
-  const at::Tensor w_out = output(where, "weights_out", a[10], shape, at::kFloat, c);
+  // A given one may have wider rows: those that the sequences' next calls take.
+  const at::Tensor w_out = a[10] == Py_None ? output(where, "weights_out", a[10], shape, at::kFloat, c) : tensor(where, "weights_out", a[10]);
+  written_rows(where, "weights_out", w_out, B, g.keep, c);
   const On on(c);
   const at::Tensor n_out = at::empty_like(lengths);
   g.weights = static_cast<const float *>(w.data_ptr());
@@ -342,6 +344,8 @@ PyObject *evict(PyObject *const *a, Py_ssize_t n) {
   g.kept = static_cast<int32_t *>(kept.data_ptr());
   g.lengths_out = static_cast<int32_t *>(n_out.data_ptr());
   g.weights_out = static_cast<float *>(w_out.data_ptr());
+  g.weights_out_stride_b = w_out.stride(0);
+  g.weights_out_stride_h = w_out.stride(1);
   check_status(attn_cache_evict(c.c, &s, &g, on.stream), where);
   return wrap({kept, n_out, w_out});
 }

@@ -76,14 +76,19 @@ bool strides_ok(int dtype, std::initializer_list<int64_t> st) {
   return true;
 }
 
-// Rows of accumulated weights that a call writes, [B, Hkv, max_pages * page_size], keep off one another.
-bool rows_apart(const attn_cache *c, const attn_cache_seqs *s, int64_t sb, int64_t sh) {
-  const int64_t room = (int64_t)s->max_pages * c->page_size;
+// Rows of accumulated weights that a call writes, [B, Hkv, room], keep off one another.
+bool rows_apart(const attn_cache *c, const attn_cache_seqs *s, int64_t sb, int64_t sh, int64_t room) {
   if (s->B <= 1) return c->Hkv <= 1 || sh >= room;
   if (c->Hkv <= 1) return sb >= room;
   const bool nested = sb >= sh;  // heads within sequences
   const int64_t in = nested ? sh : sb, out = nested ? sb : sh, count = nested ? c->Hkv : s->B;
   return in >= room && out >= (count - 1) * in + room;
+}
+int64_t table_room(const attn_cache *c, const attn_cache_seqs *s) { return (int64_t)s->max_pages * c->page_size; }
+
+// The elements from the first to behind the last of such rows.
+int64_t extent(const attn_cache *c, const attn_cache_seqs *s, int64_t sb, int64_t sh, int64_t room) {
+  return (s->B - 1) * sb + (c->Hkv - 1) * sh + room;
 }
 
 int validate(const attn_cache *c, const attn_cache_seqs *s, const attn_cache_fwd_args *a) {
@@ -98,7 +103,7 @@ int validate(const attn_cache *c, const attn_cache_seqs *s, const attn_cache_fwd
   if (!aligned4(a->weights) || !aligned4(a->weights_out) || !aligned4(a->sink)) return ATTN_ERR_INVALID;
   if (a->weights && (a->weights_stride_b < 0 || a->weights_stride_h < 0)) return ATTN_ERR_INVALID;
   if (s->B == 0 || a->Sq == 0) return ATTN_OK;
-  if (a->weights && !rows_apart(c, s, a->weights_stride_b, a->weights_stride_h)) return ATTN_ERR_INVALID;
+  if (a->weights && !rows_apart(c, s, a->weights_stride_b, a->weights_stride_h, table_room(c, s))) return ATTN_ERR_INVALID;
   if (!a->q || !aligned16(a->q)) return ATTN_ERR_INVALID;
   if (!strides_ok(a->dtype, {a->q_stride_b, a->q_stride_s, a->q_stride_h})) return ATTN_ERR_INVALID;
   const long long R = (long long)(a->Hq / c->Hkv) * a->Sq;
@@ -191,7 +196,7 @@ int attn_cache_append(const attn_cache *c, const attn_cache_seqs *s, const attn_
   if (!aligned4(a->counts) || !aligned4(a->lengths_out) || !aligned4(a->weights)) return ATTN_ERR_INVALID;
   if (a->lengths_out && a->lengths_out == s->lengths) return ATTN_ERR_INVALID;
   if (a->weights && (a->weights_stride_b < 0 || a->weights_stride_h < 0)) return ATTN_ERR_INVALID;
-  if (a->weights && !rows_apart(c, s, a->weights_stride_b, a->weights_stride_h)) return ATTN_ERR_INVALID;
+  if (a->weights && !rows_apart(c, s, a->weights_stride_b, a->weights_stride_h, table_room(c, s))) return ATTN_ERR_INVALID;
   if (a->S > 0) {
     if (!a->k || !a->v || !aligned16(a->k) || !aligned16(a->v)) return ATTN_ERR_INVALID;
     if (!strides_ok(a->dtype, {a->k_stride_b, a->k_stride_s, a->k_stride_h, a->v_stride_b, a->v_stride_s, a->v_stride_h}))
@@ -262,6 +267,14 @@ int attn_cache_evict(const attn_cache *c, const attn_cache_seqs *s, const attn_c
       !aligned4(a->weights_out))
     return ATTN_ERR_INVALID;
   if (a->weights_stride_b < 0 || a->weights_stride_h < 0 || a->lengths_out == s->lengths) return ATTN_ERR_INVALID;
+  const bool dense = a->weights_out_stride_b == 0 && a->weights_out_stride_h == 0;
+  const int64_t wo_sh = dense ? a->keep : a->weights_out_stride_h, wo_sb = dense ? (int64_t)c->Hkv * a->keep : a->weights_out_stride_b;
+  if (wo_sb < 0 || wo_sh < 0 || !rows_apart(c, s, wo_sb, wo_sh, a->keep)) return ATTN_ERR_INVALID;
+  // The selection reads weights while it writes those that stay.
+  const float *w0 = a->weights, *w1 = w0 + extent(c, s, a->weights_stride_b, a->weights_stride_h, table_room(c, s));
+  const float *o0 = a->weights_out, *o1 = o0 + extent(c, s, wo_sb, wo_sh, a->keep);
+  const bool in_place = w0 == o0 && wo_sb == a->weights_stride_b && wo_sh == a->weights_stride_h && a->keep >= table_room(c, s);
+  if (w0 < o1 && o0 < w1 && !in_place) return ATTN_ERR_INVALID;  // (in place nothing moves where nothing can be evicted)
   EvictParams p;
   memset(&p, 0, sizeof(p));
   p.c = view(c, s);
@@ -279,6 +292,8 @@ int attn_cache_evict(const attn_cache *c, const attn_cache_seqs *s, const attn_c
   p.kept = a->kept;
   p.lengths_out = a->lengths_out;
   p.weights_out = a->weights_out;
+  p.wo_sb = wo_sb;
+  p.wo_sh = wo_sh;
   return cuda_status(launch_evict(p, c->kind, reinterpret_cast<cudaStream_t>(stream)));
 }
 

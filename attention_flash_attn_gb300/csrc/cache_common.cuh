@@ -271,6 +271,7 @@ struct EvictParams {
   long long table_out_stride;
   int *kept, *lengths_out;
   float *weights_out;
+  long long wo_sb, wo_sh;
 };
 cudaError_t launch_evict(const EvictParams &p, int kind, cudaStream_t st);
 

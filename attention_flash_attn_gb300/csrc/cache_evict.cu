@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kSelThr) cache_select_kernel(const __grid_cons
     if (bad) set_status(p.c.status, kStatusBadPage);
   }
   int *kept = p.kept + (size_t)pair * p.keep;
-  float *w_out = p.weights_out + (size_t)pair * p.keep;
+  float *w_out = p.weights_out + b * p.wo_sb + h * p.wo_sh;
   const float *w = p.weights + b * p.w_sb + h * p.w_sh;
   for (int i = n + all_t; i < p.keep; i += step) {
     kept[i] = -1;

@@ -155,7 +155,11 @@ const char *attn_cache_path_name(const attn_cache *c, const attn_cache_seqs *s, 
  * reads (sequences may share pages, so an eviction in place could take another's keys).
  *   kept        [B, Hkv, keep] int32: the surviving positions, ascending, -1 past the n-th
  *   lengths_out [B] int32: n
- *   weights_out [B, Hkv, keep] float dense: their weights, 0 past the n-th
+ *   weights_out [B, Hkv, >= keep] float: their weights, 0 from the n-th to the keep-th, what lies behind
+ *               as it was.  Rows as wide as table_out (its pages times page_size) are the weights that
+ *               the sequences' next append and attention take.  May not overlap weights, nor lie
+ *               between its rows.
+ * Positions (causality, windows) count the tokens that are left from here on.
  */
 typedef struct {
     int keep, first, recent;   /* keep >= 1; first, recent >= 0; first + recent <= keep   */
@@ -165,6 +169,8 @@ typedef struct {
     int64_t table_out_stride;
     int32_t *kept, *lengths_out;
     float *weights_out;
+    int64_t weights_out_stride_b, weights_out_stride_h;  /* elements; both 0: dense [B, Hkv, keep].
+                                                            Rows of keep elements may not overlap */
 } attn_cache_evict_args;
 
 int attn_cache_evict(const attn_cache *c, const attn_cache_seqs *s, const attn_cache_evict_args *a,
