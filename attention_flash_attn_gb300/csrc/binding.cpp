@@ -265,11 +265,12 @@ void fwd_args(const char *where, const Cache &c, PyObject *const *a, attn_cache_
     weight_rows(where, "weights", w, B, room, c);
     const at::Tensor &o = a[12] == Py_None ? w : tensor(where, "weights_out", a[12]);
     written_rows(where, "weights_out", o, B, room, c);
-    if (w.strides() != o.strides()) raise(PyExc_ValueError, "%s: weights and weights_out must have the same strides", where);
+    for (int d = 0; d < 2; ++d)
+      if (stride(w, d) != stride(o, d)) raise(PyExc_ValueError, "%s: weights and weights_out must have the same strides", where);
     g->weights = static_cast<const float *>(w.data_ptr());
     g->weights_out = static_cast<float *>(o.data_ptr());
-    g->weights_stride_b = w.stride(0);
-    g->weights_stride_h = w.stride(1);
+    g->weights_stride_b = stride(w, 0);
+    g->weights_stride_h = stride(w, 1);
   } else if (a[12] != Py_None) {
     raise(PyExc_ValueError, "%s: weights_out needs weights", where);
   }
