@@ -42,18 +42,41 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _stamp() -> str:
+def _hash(files, *words) -> str:
     h = hashlib.sha256()
-    files = _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")))
-    files += sorted(glob.glob(os.path.join(ROOT, "include", "*.h")))
     for f in files:
         h.update(os.path.relpath(f, ROOT).encode())  # relative: the same sources hash alike anywhere
         with open(f, "rb") as fh:
             h.update(fh.read())
-    with open(BINDING_SRC, "rb") as fh:
-        h.update(fh.read())
-    h.update(" ".join(ARCH + FLAGS + [torch.__version__, sys.version]).encode())
+    h.update(" ".join(words).encode())
     return h.hexdigest()
+
+
+def _headers():
+    return sorted(glob.glob(os.path.join(ROOT, "include", "*.h")))
+
+
+def _stamp() -> str:
+    """Of the library: its sources and flags."""
+    own = sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")))
+    return _hash(_sources() + own + _headers(), *ARCH, *FLAGS)
+
+
+def _binding_stamp() -> str:
+    """Of the binding: its source, the PyTorch and the Python that it is compiled for."""
+    return _hash([BINDING_SRC] + _headers(), torch.__version__, sys.version)
+
+
+def _current(path: str, stamp_file: str, stamp: str) -> bool:
+    if not os.path.exists(path) or not os.path.exists(stamp_file):
+        return False
+    with open(stamp_file) as fh:
+        return fh.read() == stamp
+
+
+def _write(path: str, text: str) -> None:
+    with open(path, "w") as fh:
+        fh.write(text)
 
 
 # Sources that the backward main kernel's code depends on: a DRAM-traffic figure recorded by
@@ -123,15 +146,29 @@ def _link_binding(obj: str) -> None:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile (if sources changed) and return the path of the shared library."""
+    """Compile what has changed and return the path of the shared library.  The library needs nvcc alone; it is linked
+    before a failure of the binding's compilation (which needs PyTorch's headers) is raised."""
     os.makedirs(BUILD, exist_ok=True)
-    stamp_file = os.path.join(BUILD, "stamp")
-    stamp = _stamp()
-    if not force and os.path.exists(LIB) and os.path.exists(BINDING) and os.path.exists(stamp_file):
-        if open(stamp_file).read() == stamp:
-            return LIB
-    nvcc = _nvcc()
+    lib_stamp, binding_stamp = (os.path.join(BUILD, n) for n in ("stamp", "stamp_binding"))
+    make_lib = force or not _current(LIB, lib_stamp, _stamp())
+    make_binding = force or not _current(BINDING, binding_stamp, _binding_stamp())
+    binding_obj = os.path.join(BUILD, "binding.o")
     srcs = _sources()
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        binding = ex.submit(_compile_binding, binding_obj) if make_binding else None
+        if make_lib:
+            _build_lib(ex, srcs, verbose)
+            _write(lib_stamp, _stamp())
+        if binding:
+            binding.result()
+    if make_binding:
+        _link_binding(binding_obj)
+        _write(binding_stamp, _binding_stamp())
+    return LIB
+
+
+def _build_lib(ex, srcs, verbose: bool) -> None:
+    nvcc = _nvcc()
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
@@ -141,14 +178,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    binding_obj = os.path.join(BUILD, "binding.o")
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
-        binding = ex.submit(_compile_binding, binding_obj)
-        results = list(ex.map(compile_one, srcs))
-        binding.result()
+    results = list(ex.map(compile_one, srcs))
     log = "\n".join(err for _, err in results)
-    with open(os.path.join(BUILD, "ptxas.log"), "w") as fh:
-        fh.write(log)
+    _write(os.path.join(BUILD, "ptxas.log"), log)
     if verbose:
         print(log)
     tmp = LIB + f".tmp{os.getpid()}"
@@ -157,10 +189,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding_obj)
-    with open(stamp_file, "w") as fh:
-        fh.write(stamp)
-    return LIB
 
 
 if __name__ == "__main__":
