@@ -116,7 +116,7 @@ int validate(const attn_cache *c, const attn_cache_seqs *s, const attn_cache_fwd
 }
 
 bool use_tc(const attn_cache *c, const attn_cache_seqs *s, const attn_cache_fwd_args *a) {
-  return tc_supported_rows(a->dtype, c->D, (int)std::min((long long)INT_MAX, (long long)(a->Hq / c->Hkv) * a->Sq), s->B);
+  return tc_supported_rows(a->dtype, c->D, (int)std::min((long long)INT_MAX, (long long)(a->Hq / c->Hkv) * a->Sq), s->B, c->Hkv);
 }
 bool use_mma(const attn_cache *c) { return mma_supported(c->D); }
 

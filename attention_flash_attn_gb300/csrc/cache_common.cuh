@@ -206,7 +206,7 @@ cudaError_t launch_fwd_mma(const FwdParams &p, int dtype, int kind, cudaStream_t
 cudaError_t launch_mma_e4m3(const FwdParams &p, int dtype, cudaStream_t st);
 cudaError_t launch_mma_int8(const FwdParams &p, int dtype, cudaStream_t st);
 // tcgen05 path (many rows).
-bool tc_supported_rows(int dtype, int D, int R, int B);
+bool tc_supported_rows(int dtype, int D, int R, int B, int Hkv);
 int tc_row_tile();
 int tc_unit_shift();
 int tc_splits(const FwdParams &p);

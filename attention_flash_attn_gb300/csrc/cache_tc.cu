@@ -661,14 +661,23 @@ template <int KIND, int D> cudaError_t launch_t(const FwdParams &p, cudaStream_t
 int tc_row_tile() { return kBM; }
 int tc_unit_shift() { return 7; }
 
-// From how many rows per kv head this kernel is taken.  Measured against the kernel of cache_mma.cuh (us, this /
-// that) with 8 kv heads.  D = 128: 16 ragged rows up to 8192 keys, 36 query rows 128 / 98, 64 131 / 109, 96
-// 136 / 159, 128 141 / 209; one row of 16111 keys, 64 rows 24 / 28 (with a cap 32 / 30), 2048 186 / 430; one of
-// 3000, 64 rows 17 / 16.  D = 64, where a tile's MMAs are half and its softmax is not: the ragged rows, 160 query
-// rows 49 / 37, 512 78 / 72, 1024 125 / 129, 2048 193 / 244; one row of 16111 keys, 128 rows 21 / 26 (with a cap
-// 29 / 31), 256 31 / 47, 512 50 / 71; one of 3000, 128 rows 16 / 13, 256 20 / 16, 384 23 / 22, 512 20 / 23.  A head
-// dim in between takes the time of the next larger one on either.
-bool tc_supported_rows(int dtype, int D, int R, int B) { return dtype == kBF16 && D <= 128 && R > (D > 64 ? 64 : B > 1 ? 512 : 256); }
+// When this kernel is taken instead of that of cache_mma.cuh.  Both measured (us, that one / this one; 4 query heads to each of
+// 8 kv heads; ragged rows up to the keys given).
+// D = 128, from 65 rows per kv head: 16 sequences of 8192 keys, 48 rows 106 / 90, 64 111 / 91 (with a cap 120 / 137), 96
+// 159 / 97; 4 of 3000, 64 rows 22 / 29, 96 33 / 33; one of 16111, 64 rows 29 / 23 (cap 31 / 32), 96 39 / 24; one of 3000, 96
+// 17 / 18.
+// D = 64, where a tile's MMAs are half and its softmax is not: a batch from 65 rows on if the other kernel's tiles of
+// 32 rows do not fit one wave of two CTAs per SM (8 kv heads x 16 sequences x 3 tiles do not), else from 513 on.  16 of
+// 8192, 64 rows 65 / 79, 96 97 / 82, 128 125 / 86 (cap 145 / 135), 512 447 / 228; 16 of 1000, 64 17 / 27, 96 47 / 30; 64 of 1000,
+// 96 126 / 54; 4 of 3000, 128 22 / 32, 256 37 / 52, 384 58 / 71, 512 71 / 56; 4 of 8192, 256 66 / 69, 512 128 / 84.  A single
+// sequence from 257 rows on: 16111 keys, 128 rows 26 / 21 (cap 31 / 29), 256 48 / 32, 512 74 / 50; 3000, 128 13 / 16, 256 16 / 19, 384
+// 23 / 22, 512 23 / 20.
+// A head dim in between takes the time of the next larger one on either.
+bool tc_supported_rows(int dtype, int D, int R, int B, int Hkv) {
+  if (dtype != kBF16 || D > 128 || R <= 64) return false;
+  if (D > 64) return true;
+  return R > (B > 1 ? 512 : 256) || (B > 1 && (long long)B * Hkv * ((R + 31) / 32) > 2LL * device_sm_count());
+}
 
 // Shares of an item's keys, one CTA each, one CTA per SM, of at least four tiles.  One sequence: as many as end first,
 // by a count of tiles (kStart: a CTA's start and end).  A batch, whose lengths the host does not know: enough for
