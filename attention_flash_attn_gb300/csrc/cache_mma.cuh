@@ -19,10 +19,11 @@
 //     2^14, so that the many small probabilities beside a large one keep their bits down to 2^-28 of it (held
 //     as they are, from 2^-14 on they did not, and below 2^-25 they were 0, while the sum counted them).
 //   - float queries take the same way in two terms each: q = hi + lo in fp16 (22 bits), p 2^14 = hi + lo, both
-//     terms multiplied into the same accumulators.  Twice the MMAs; the FFMA kernel took 39 us where this
-//     takes 16 (9 ragged rows up to 9001 keys, one kv head).
-// Measured at 4 rows of some 115,000 keys, 8 kv heads, 4 bf16 queries to each: 4.9 TB/s at D = 64, 6.0 at 128, 6.5
-// at 256 (a copy reaches 6.8); float queries at D = 128 5.1.  Short calls are bound by the fixed parts, some 12 us:
+//     terms multiplied into the same accumulators.  Twice the MMAs; a call on the FFMA kernel took 39 us where
+//     it took 26 with this one, now 25 (9 ragged rows up to 9001 keys, one kv head, a join and a weights pass in each).
+// Measured at 4 rows of some 115,000 keys, 8 kv heads, 4 bf16 queries to each: 5.0 TB/s at D = 64, 6.0 at 128, 6.5
+// at 256 (a copy reaches 6.8); float queries at D = 128 5.3.  Registers: most forms of 64 and 128 columns spill, up to
+// 92 bytes a thread, within what two or three CTAs to an SM leave them.  Short calls are bound by the fixed parts, some 12 us:
 // launch, plan and first loads, the last run's end, the join.  With a row tile of 32, or D = 64 (half the bytes
 // per score), the warps' issue slots and latencies bound it, not the memory.
 #pragma once

@@ -2,7 +2,7 @@
 // and 128 columns, those past the head dim filled with zeros), many query rows per kv head (drafts of several
 // tokens, chunks of a prompt, many heads to a kv head).
 //
-// m16n8k16 products end at some 330 TFLOP/s here; with many rows the tensor cores' own path does more (715 TFLOP/s
+// m16n8k16 products end at some 300 TFLOP/s here; with many rows the tensor cores' own path does more (730 TFLOP/s
 // for 2048 rows of 16111 keys at D = 128, 410 at D = 64).  One CTA computes one 128-row tile of one (sequence, kv
 // head) over one share of its keys, in tiles of 128 keys:
 //   warp 0        TMA: the tile's codes of K and V, page by page, and the scales of its 16-key groups into a
@@ -19,7 +19,8 @@
 // registers moved to the softmax (640 threads), and converters for K and V apart were slower (258 and 270 us
 // against 233): shared memory is what they share.  So was a form of 256 rows to a CTA, each of whose two groups of
 // warps had 128 rows or every second tile, with scores in one buffer each: 176 us where this took 194 without a
-// cap, but 405 against 342 with one, and 47 against 43 at 256 rows.
+// cap, but 405 against 342 with one, and 47 against 43 at 256 rows.  At 128 columns the softmax warps spill: 128 registers
+// are what 448 threads leave, and 152 (e4m3) or 232 bytes a thread (int8) go to local memory.
 #include <algorithm>
 
 #include "cache_work.cuh"
