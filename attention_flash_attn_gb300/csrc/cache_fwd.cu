@@ -385,12 +385,12 @@ __global__ void __launch_bounds__(kThreads) cache_weights_kernel(const __grid_co
   }
   grid_wait();
   if (j0 >= len || (!any && p.w_in == p.w_out)) return;
-  const int r1 = any ? i1 * p.G : 0;
-  const float *row = scores_row(p, b, hk, i0 * p.G) + j0;
+  const int first = any ? i0 * p.G : 0, r1 = any ? i1 * p.G : 0;  // rows
+  const float *row = scores_row(p, b, hk, first) + j0;
   const float *lse = p.LSE + ((size_t)b * p.Hq + hk * p.G) * p.Sq;
   int query = i0, head = 0;  // of row r0 + i
 #pragma unroll 1
-  for (int r0 = i0 * p.G; r0 < r1; r0 += 4, row += 4 * p.Lpad) {
+  for (int r0 = first; r0 < r1; r0 += 4, row += 4 * p.Lpad) {
     // Scores are stored for the keys that some row of the tile sees (a superset of what a row sees); the others, and
     // the last row's in place of those past it, are loaded too, unconditionally so that all loads go out at once (behind
     // conditions each waited for the one before: 86 sequences of 135 keys, 16 heads, 15 rows, 20 us for this pass
