@@ -114,7 +114,8 @@ int attn_cache_append(const attn_cache *c, const attn_cache_seqs *s, const attn_
  * 128 take tcgen05 products.  What is rounded is a probability times its value's scale: half a step
  * is 2^-11 of it down to 2^-28 (tcgen05: 2^-25) of the row's largest such product, and below 2^-39
  * (2^-36) of that largest one.  Larger head dims run on fp32 FFMA kernels; there the products are
- * 0 below 2^-149 of the largest.  Logit and log2(scale) are added in float: a scale 2^e costs |e| 2^-24.  Long key ranges are split
+ * 0 below 2^-149 of the largest.  Logit and log2(scale) are added in float: a scale of 2^e costs
+ * |e| 2^-24 of each probability.  Long key ranges are split
  * over CTAs and joined in a fixed order; how, depends on the shapes and the lengths alone.
  */
 typedef struct {
